@@ -437,6 +437,65 @@ moe_status_t moe_get_config(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
 /* Number of entries of the table compiled into the library. */
 int32_t moe_builtin_config_count(void);
 
+/* ---- around the expert forward: norms, gate and scaled residual ----------
+ * The RMS norm before a block and the one after it, with the block's gate and the
+ * scaled residual, over the rows of [T, H] tensors (the layer the pages' expert forward
+ * sits in; they print no norm themselves):
+ *   before:  out[t] = x[t] r_t weight,                         r_t = 1 / sqrt(mean_h x[t]^2 + eps)
+ *   after:   out[t] = residual_scale residual[t] + a(gate) y[t] r_t weight,  r_t of y
+ *            and, on request in the same pass, the next block's norm of that sum:
+ *            next_out[t] = out[t] r'_t next_weight               r'_t of out before it is rounded
+ * Row tensors are bf16 or f32, each by itself, any strides; arithmetic is fp32 and each
+ * output is rounded once.  Rows with inner stride 1, 16-byte aligned starts and H a
+ * multiple of 8 are moved 16 bytes at a time, others element by element.
+ *   weight, next_weight  [H] bf16 or f32, any stride; NULL = ones
+ *   gate       [T or 1, H or 1] bf16 or f32, any strides, broadcast over its axes of size 1;
+ *              NULL = 1.  gate_act: the function a applied to it
+ *   residual   NULL, or residual_scale 0, leaves it out (its infinities too)
+ *   normalize  0: the norm of y is left out (r_t = 1), weight and gate still apply
+ *   rstd, next_rstd  [T] f32, any stride: r_t and r'_t (what the gradient reads); NULL: not wanted
+ * out may be the same tensor (same strides) as x, y or residual; other overlaps are not
+ * allowed.  eps finite and >= 0; squares are summed in fp32, so |x| has to stay below about 1e18.
+ * 1 <= H <= 16384; T = 0 is a no-op.  next_out needs no next_rstd and the other way round;
+ * next_weight is read with next_out only.  Asynchronous on `stream`, no allocation, no state
+ * between calls; every pointer is of the current device. */
+enum { MOE_GATE_NONE = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_TANH = 2 };
+
+moe_status_t moe_norm_before(const moe_tensor_t* x, const moe_tensor_t* weight, float eps,
+                             moe_tensor_t* out, moe_tensor_t* rstd, moe_stream_t stream);
+moe_status_t moe_norm_after(const moe_tensor_t* y, const moe_tensor_t* residual,
+                            const moe_tensor_t* weight, const moe_tensor_t* gate, int32_t gate_act,
+                            int32_t normalize, float residual_scale, float eps, moe_tensor_t* out,
+                            moe_tensor_t* rstd, const moe_tensor_t* next_weight,
+                            moe_tensor_t* next_out, moe_tensor_t* next_rstd, moe_stream_t stream);
+
+/* Their gradients, from the rstd that the forward wrote.  With h = x r:
+ *   before:  dx = residual_scale residual_grad + r (p - h mean_h(p h)),  p = dout weight
+ *            dweight = sum_t dout h
+ * (residual_grad is the gradient that reaches x past the block: the dout of the norm after
+ * it; NULL or residual_scale 0 leaves it out), and with h = y r, d = dout a(gate):
+ *   after:   dy = r (p - h mean_h(p h)),  p = d weight   (normalize 0: dy = p, h = y)
+ *            dweight = sum_t d h
+ *            dgate = sum over the gate's broadcast axes of dout h weight a'(gate)
+ * The gradient with respect to residual is residual_scale dout: residual_grad above applies it.
+ *   rstd     [T] f32 (after, normalize 0: not read, may be NULL)
+ *   dweight  [H] f32 or bf16, any stride; NULL: not wanted
+ *   dgate    the gate's sizes, f32 or bf16, any strides; NULL: not wanted
+ * Column sums are fp32, in a fixed order: the same call gives the same bits.  dx / dy may be the
+ * same tensor as an input of its shape.  `workspace`: moe_norm_backward_workspace_bytes(T, H),
+ * 256-byte aligned.  T = 0 writes zeros to dweight and dgate. */
+size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t H);
+moe_status_t moe_norm_before_backward(const moe_tensor_t* dout, const moe_tensor_t* x,
+                                      const moe_tensor_t* rstd, const moe_tensor_t* weight,
+                                      const moe_tensor_t* residual_grad, float residual_scale,
+                                      moe_tensor_t* dx, moe_tensor_t* dweight, void* workspace,
+                                      size_t workspace_bytes, moe_stream_t stream);
+moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_t* y,
+                                     const moe_tensor_t* rstd, const moe_tensor_t* weight,
+                                     const moe_tensor_t* gate, int32_t gate_act, int32_t normalize,
+                                     moe_tensor_t* dy, moe_tensor_t* dweight, moe_tensor_t* dgate,
+                                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* Library version string. */
 const char* moe_version(void);
 

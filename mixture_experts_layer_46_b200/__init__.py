@@ -13,3 +13,5 @@ from ._abi import (MoeConfig, MoeError, MoeTensor, MoeW13, align, builtin_config
                    workspace_bytes, workspace_layout, debug_capture, MOE_CAPTURE_H_PREQUANT,
                    measure_mma_peak, backward, backward_input, backward_status, backward_workspace_bytes,
                    transpose_experts, host_workspace_bytes)
+from .block import (norm_after, norm_after_backward, norm_backward_workspace_bytes, norm_before,  # noqa: F401
+                    norm_before_backward)

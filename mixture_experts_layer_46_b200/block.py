@@ -1,0 +1,185 @@
+"""The operators around the expert forward (include/moe.h): the norms before and after a
+block with its gate and scaled residual, and their gradients.
+
+Argument marshalling only, as in _abi.py.  Tensors that a call makes for its caller are
+allocated on the stream it runs on, on the inputs' device; every tensor of a call has to be on
+that one device.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import struct
+
+import torch
+
+from ._abi import MOE_BF16, MOE_F32, MOE_I32, MOE_I64, _check, load
+
+GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
+
+_DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.int32: MOE_I32, torch.int64: MOE_I64}
+# moe_tensor_t: data, dtype, ndim, sizes[4], strides[4], scale, scale_strides[4]
+_TENSOR = struct.Struct("=Qii4q4qQ4q").pack
+_PAD = (0, 0, 0, 0)
+
+
+def _desc(t: torch.Tensor | None):
+    """The bytes of a moe_tensor_t (None stays NULL); unknown dtypes are rejected by the library."""
+    if t is None:
+        return None
+    n = t.dim()
+    if n > 4:
+        raise ValueError(f"a tensor of {n} dimensions")
+    pad = _PAD[n:]
+    return _TENSOR(t.data_ptr(), _DT.get(t.dtype, 99), n, *t.shape, *pad, *t.stride(), *pad, 0, 0, 0, 0, 0)
+
+
+class _Call:
+    """The device and stream of a call: checks that the tensors share one CUDA device, makes it
+    current and, with a stream of its own, makes that the stream new tensors belong to."""
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors on {dev} and on {t.device}")
+        if dev.type != "cuda":
+            raise ValueError(f"a tensor on {dev}: the operators run on a CUDA device only")
+        self.device, self._stack = dev, None
+        if stream is None and dev.index == torch.cuda.current_device():
+            self.stream = torch.cuda.current_stream(dev).cuda_stream
+            return
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+        self._stack = contextlib.ExitStack()
+        self._stack.enter_context(torch.cuda.device(dev))
+        if stream is not None:
+            self._stack.enter_context(torch.cuda.stream(stream))
+        self.stream = torch.cuda.current_stream(dev).cuda_stream
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self._stack is not None:
+            self._stack.close()
+        return False
+
+    def empty(self, *shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, given, need):
+        if given is None:
+            return torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
+        return given
+
+
+def _act(name: str) -> int:
+    if name not in GATE_ACTS:
+        raise ValueError(f"gate_act {name!r}: one of {', '.join(GATE_ACTS)}")
+    return GATE_ACTS[name]
+
+
+def _rows(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} has {t.dim()} dimensions, not 2")
+    return t.shape
+
+
+def norm_before(x, weight=None, *, eps=1e-6, out=None, out_dtype=None, rstd=None, stream=None):
+    """(out, rstd): out[t] = x[t] * rstd[t] * weight, rstd[t] = 1 / sqrt(mean(x[t]^2) + eps).
+
+    x [T, H] bf16 or f32, any strides; out in out_dtype (x's by default)."""
+    T, H = _rows(x, "x")
+    with _Call(stream, x, weight, out, rstd) as c:
+        if out is None:
+            out = c.empty(T, H, dtype=out_dtype or x.dtype)
+        if rstd is None:
+            rstd = c.empty(T, dtype=torch.float32)
+        _check(load().moe_norm_before(_desc(x), _desc(weight), eps, _desc(out), _desc(rstd), c.stream),
+               "moe_norm_before")
+    return out, rstd
+
+
+def norm_after(y, residual=None, weight=None, gate=None, *, gate_act="none", normalize=True, residual_scale=1.0,
+               eps=1e-6, out=None, out_dtype=None, rstd=None, next_norm=None, next_weight=None, next_out=None,
+               next_dtype=None, next_rstd=None, stream=None):
+    """out = residual_scale * residual + a(gate) * y * rstd * weight, and with a next norm
+    (next_norm=True, or next_weight or next_out given) that sum's own norm in the same pass.
+
+    Returns (out, rstd), or (out, rstd, next_out, next_rstd) with a next norm.  gate is
+    [T or 1, H or 1]; out takes the residual's dtype (y's without one) and next_out out's,
+    unless out_dtype / next_dtype say otherwise.  With normalize=False the norm of y is left
+    out and rstd is ones."""
+    T, H = _rows(y, "y")
+    act = _act(gate_act)
+    if next_norm is None:
+        next_norm = next_weight is not None or next_out is not None or next_rstd is not None
+    with _Call(stream, y, residual, weight, gate, out, rstd, next_weight, next_out, next_rstd) as c:
+        if out is None:
+            out = c.empty(T, H, dtype=out_dtype or (y if residual is None else residual).dtype)
+        if rstd is None:
+            rstd = c.empty(T, dtype=torch.float32)
+        if next_norm and next_out is None:
+            next_out = c.empty(T, H, dtype=next_dtype or out.dtype)
+        if next_norm and next_rstd is None:
+            next_rstd = c.empty(T, dtype=torch.float32)
+        _check(load().moe_norm_after(_desc(y), _desc(residual), _desc(weight), _desc(gate), act,
+                                     1 if normalize else 0, residual_scale, eps, _desc(out), _desc(rstd),
+                                     _desc(next_weight), _desc(next_out), _desc(next_rstd), c.stream),
+               "moe_norm_after")
+    return (out, rstd, next_out, next_rstd) if next_norm else (out, rstd)
+
+
+def norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(load().moe_norm_backward_workspace_bytes(T, H))
+
+
+def norm_before_backward(dout, x, rstd, weight=None, *, residual_grad=None, residual_scale=1.0, dx=None,
+                         dweight=None, weight_grad=True, grad_dtype=torch.float32, workspace=None, stream=None):
+    """(dx, dweight): the gradient of norm_before given dout, plus residual_scale *
+    residual_grad, the gradient that reaches x past the block.  dweight (in grad_dtype) is None
+    without a weight or with weight_grad=False."""
+    T, H = _rows(dout, "dout")
+    want = dweight is not None or (weight is not None and weight_grad)
+    with _Call(stream, dout, x, rstd, weight, residual_grad, dx, dweight, workspace) as c:
+        if dx is None:
+            dx = c.empty(T, H, dtype=x.dtype)
+        if want and dweight is None:
+            dweight = c.empty(H, dtype=grad_dtype)
+        ws = c.workspace(workspace, norm_backward_workspace_bytes(T, H)) if want else None
+        _check(load().moe_norm_before_backward(
+            _desc(dout), _desc(x), _desc(rstd), _desc(weight), _desc(residual_grad), residual_scale, _desc(dx),
+            _desc(dweight), ws.data_ptr() if want else None, ws.numel() * ws.element_size() if want else 0, c.stream),
+            "moe_norm_before_backward")
+    return dx, dweight
+
+
+def norm_after_backward(dout, y, rstd, weight=None, gate=None, *, gate_act="none", normalize=True, dy=None,
+                        dweight=None, dgate=None, weight_grad=True, gate_grad=True, grad_dtype=torch.float32,
+                        workspace=None, stream=None):
+    """(dy, dweight, dgate): the gradient of norm_after given dout, rstd as the forward wrote it.
+    dweight and dgate (in grad_dtype; dgate of the gate's shape, summed over its axes of size
+    1) are None without a weight or a gate, or with weight_grad / gate_grad False.  The gradient
+    with respect to the residual is residual_scale * dout (norm_before_backward adds it)."""
+    T, H = _rows(dout, "dout")
+    act = _act(gate_act)
+    want_w = dweight is not None or (weight is not None and weight_grad)
+    want_g = dgate is not None or (gate is not None and gate_grad)
+    with _Call(stream, dout, y, rstd, weight, gate, dy, dweight, dgate, workspace) as c:
+        if dy is None:
+            dy = c.empty(T, H, dtype=y.dtype)
+        if want_w and dweight is None:
+            dweight = c.empty(H, dtype=grad_dtype)
+        if want_g and dgate is None:
+            dgate = c.empty(*gate.shape, dtype=grad_dtype)
+        want = want_w or want_g
+        ws = c.workspace(workspace, norm_backward_workspace_bytes(T, H)) if want else None
+        _check(load().moe_norm_after_backward(
+            _desc(dout), _desc(y), _desc(rstd), _desc(weight), _desc(gate), act, 1 if normalize else 0, _desc(dy),
+            _desc(dweight), _desc(dgate), ws.data_ptr() if want else None,
+            ws.numel() * ws.element_size() if want else 0, c.stream),
+            "moe_norm_after_backward")
+    return dy, dweight, dgate

@@ -13,6 +13,7 @@
 #include <unordered_map>
 
 #include "../../include/moe.h"
+#include "moe_block.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -325,6 +326,23 @@ moe_status_t cached_workspace(size_t need, void** ptr) {
 }
 
 }  // namespace
+
+// what the entry points in other files need of the above
+moe_status_t api_device(int* num_sms, DeviceErrors** err) {
+  DeviceInfo* d = nullptr;
+  const moe_status_t s = device_info(&d);
+  if (s != MOE_OK) return s;
+  *num_sms = d->num_sms;
+  if (err) *err = d->errors;
+  return MOE_OK;
+}
+moe_status_t api_cuda_fail(cudaError_t rc, const char* where) { return cuda_fail(rc, where); }
+moe_status_t api_make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base,
+                          const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                          CUtensorMapSwizzle swz) {
+  return make_map(map, dt, rank, base, dims, strides_bytes, box, swz);
+}
+void api_set_launches(int32_t n) { t_last_launches = n; }
 
 // ---------------------------------------------------------------- layout
 

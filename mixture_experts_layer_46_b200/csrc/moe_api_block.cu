@@ -1,0 +1,284 @@
+// Entry points of the operators around the expert forward (include/moe.h): argument
+// checks, views and launches.  Every error is found before anything is launched.
+#include <cmath>
+
+#include "../../include/moe.h"
+#include "moe_block.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+int64_t float_size(int32_t dt) { return dt == MOE_BF16 ? 2 : dt == MOE_F32 ? 4 : 0; }
+
+// A float row tensor [T, H]: MOE_OK and its view, or what is wrong with it.
+moe_status_t rows_of(const moe_tensor_t* t, int64_t T, int64_t H, bool output, RowView* v) {
+  if (t->ndim != 2) return MOE_ERR_INVALID_ARG;
+  if (float_size(t->dtype) == 0) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (t->sizes[0] != T || t->sizes[1] != H) return MOE_ERR_SHAPE_MISMATCH;
+  if (T > 0 && H > 0 && !t->data) return MOE_ERR_INVALID_ARG;
+  // rows or columns on top of one another cannot be written
+  if (output && ((T > 1 && t->strides[0] == 0) || (H > 1 && t->strides[1] == 0)))
+    return MOE_ERR_UNSUPPORTED_LAYOUT;
+  v->data = t->data;
+  v->s0 = t->strides[0];
+  v->s1 = t->strides[1];
+  v->dtype = t->dtype;
+  return MOE_OK;
+}
+
+// A weight vector [H] (null: ones).
+moe_status_t vector_of(const moe_tensor_t* t, int64_t n, bool output, RowView* v) {
+  *v = RowView();
+  if (!t) return MOE_OK;
+  if (t->ndim != 1 || !t->data) return MOE_ERR_INVALID_ARG;
+  if (float_size(t->dtype) == 0) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (t->sizes[0] != n) return MOE_ERR_SHAPE_MISMATCH;
+  if (output && n > 1 && t->strides[0] == 0) return MOE_ERR_UNSUPPORTED_LAYOUT;
+  v->data = t->data;
+  v->s1 = t->strides[0];
+  v->dtype = t->dtype;
+  return MOE_OK;
+}
+
+// A [T] f32 vector (null allowed unless required).
+moe_status_t rstd_of(const moe_tensor_t* t, int64_t T, bool output, float** p, int64_t* s) {
+  *p = nullptr;
+  *s = 0;
+  if (!t) return MOE_OK;
+  if (t->ndim != 1) return MOE_ERR_INVALID_ARG;
+  if (t->dtype != MOE_F32) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (t->sizes[0] != T) return MOE_ERR_SHAPE_MISMATCH;
+  if (T > 0 && !t->data) return MOE_ERR_INVALID_ARG;
+  if (output && T > 1 && t->strides[0] == 0) return MOE_ERR_UNSUPPORTED_LAYOUT;
+  *p = static_cast<float*>(t->data);
+  *s = t->strides[0];
+  return MOE_OK;
+}
+
+// A gate broadcast over its axes of size 1 (null: none).
+moe_status_t gate_of(const moe_tensor_t* t, int64_t T, int64_t H, int32_t act, RowView* v, int* mode) {
+  *v = RowView();
+  *mode = kGateNone;
+  if (act != MOE_GATE_NONE && act != MOE_GATE_SIGMOID && act != MOE_GATE_TANH) return MOE_ERR_INVALID_ARG;
+  if (!t) return MOE_OK;
+  if (t->ndim != 2) return MOE_ERR_INVALID_ARG;
+  if (float_size(t->dtype) == 0) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if ((t->sizes[0] != T && t->sizes[0] != 1) || (t->sizes[1] != H && t->sizes[1] != 1))
+    return MOE_ERR_SHAPE_MISMATCH;
+  if (t->sizes[0] > 0 && !t->data) return MOE_ERR_INVALID_ARG;
+  v->data = t->data;
+  v->s0 = t->sizes[0] == 1 ? 0 : t->strides[0];
+  v->s1 = t->sizes[1] == 1 ? 0 : t->strides[1];
+  v->dtype = t->dtype;
+  *mode = t->sizes[0] == 1 ? (t->sizes[1] == 1 ? kGateOne : kGateChannel)
+                           : (t->sizes[1] == 1 ? kGateToken : kGateFull);
+  return MOE_OK;
+}
+
+// 16-byte accesses possible: unit inner stride, aligned rows (or no tensor at all).
+bool wide_ok(const RowView& v) {
+  if (!v.data) return true;
+  return v.s1 == 1 && reinterpret_cast<uintptr_t>(v.data) % 16 == 0 && (v.s0 * float_size(v.dtype)) % 16 == 0;
+}
+
+bool norm_shape_ok(const moe_tensor_t* t, float eps) {
+  return t && t->ndim == 2 && t->sizes[0] >= 0 && t->sizes[1] >= 1 && t->sizes[1] <= kNormMaxH &&
+         t->sizes[0] < (int64_t(1) << 40) && std::isfinite(eps) && eps >= 0.0f;
+}
+
+#define MOE_TRY(call)                   \
+  do {                                  \
+    const moe_status_t _s = (call);     \
+    if (_s != MOE_OK) return _s;        \
+  } while (0)
+
+size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_norm_before(const moe_tensor_t* x, const moe_tensor_t* weight, float eps,
+                             moe_tensor_t* out, moe_tensor_t* rstd, moe_stream_t stream) {
+  if (!out || !norm_shape_ok(x, eps)) return MOE_ERR_INVALID_ARG;
+  NormBefore g;
+  g.T = x->sizes[0];
+  g.H = static_cast<int>(x->sizes[1]);
+  g.eps = eps;
+  MOE_TRY(rows_of(x, g.T, g.H, false, &g.x));
+  MOE_TRY(rows_of(out, g.T, g.H, true, &g.out));
+  MOE_TRY(vector_of(weight, g.H, false, &g.w));
+  MOE_TRY(rstd_of(rstd, g.T, true, &g.rstd, &g.rstd_s));
+  if (g.T == 0) return MOE_OK;
+  int sms = 0;
+  MOE_TRY(api_device(&sms, nullptr));
+  const bool wide = g.H % 8 == 0 && wide_ok(g.x) && wide_ok(g.out) && wide_ok(g.w);
+  const cudaError_t rc = launch_norm_before(g, wide, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_before");
+  api_set_launches(1);
+  return MOE_OK;
+}
+
+moe_status_t moe_norm_after(const moe_tensor_t* y, const moe_tensor_t* residual,
+                            const moe_tensor_t* weight, const moe_tensor_t* gate, int32_t gate_act,
+                            int32_t normalize, float residual_scale, float eps, moe_tensor_t* out,
+                            moe_tensor_t* rstd, const moe_tensor_t* next_weight,
+                            moe_tensor_t* next_out, moe_tensor_t* next_rstd, moe_stream_t stream) {
+  if (!out || !norm_shape_ok(y, eps) || (normalize != 0 && normalize != 1)) return MOE_ERR_INVALID_ARG;
+  NormAfter g;
+  g.T = y->sizes[0];
+  g.H = static_cast<int>(y->sizes[1]);
+  g.eps = eps;
+  g.alpha = residual_scale;
+  g.normalize = normalize;
+  g.act = gate_act;
+  MOE_TRY(rows_of(y, g.T, g.H, false, &g.y));
+  if (residual) MOE_TRY(rows_of(residual, g.T, g.H, false, &g.x));
+  if (residual_scale == 0.0f) g.x = RowView();
+  MOE_TRY(rows_of(out, g.T, g.H, true, &g.out));
+  MOE_TRY(vector_of(weight, g.H, false, &g.w));
+  int mode = kGateNone;
+  MOE_TRY(gate_of(gate, g.T, g.H, gate_act, &g.gate, &mode));
+  g.gate_one_col = mode == kGateToken || mode == kGateOne;
+  MOE_TRY(rstd_of(rstd, g.T, true, &g.rstd, &g.rstd_s));
+  MOE_TRY(vector_of(next_weight, g.H, false, &g.wn));
+  if (next_out) MOE_TRY(rows_of(next_out, g.T, g.H, true, &g.nxt));
+  MOE_TRY(rstd_of(next_rstd, g.T, true, &g.next_rstd, &g.next_rstd_s));
+  if (g.T == 0) return MOE_OK;
+  int sms = 0;
+  MOE_TRY(api_device(&sms, nullptr));
+  const bool wide = g.H % 8 == 0 && wide_ok(g.y) && wide_ok(g.x) && wide_ok(g.out) && wide_ok(g.w) &&
+                    (g.gate_one_col || wide_ok(g.gate)) && (!next_out || (wide_ok(g.wn) && wide_ok(g.nxt)));
+  const cudaError_t rc = launch_norm_after(g, wide, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_after");
+  api_set_launches(1);
+  return MOE_OK;
+}
+
+size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t H) {
+  if (T < 0 || H < 1 || H > kNormMaxH) return 0;
+  const size_t rows = static_cast<size_t>(norm_backward_rows(T, H, kNormMaxSms));
+  return 2 * round256((rows > 0 ? rows : 1) * static_cast<size_t>(H) * sizeof(float));
+}
+
+moe_status_t moe_norm_before_backward(const moe_tensor_t* dout, const moe_tensor_t* x,
+                                      const moe_tensor_t* rstd, const moe_tensor_t* weight,
+                                      const moe_tensor_t* residual_grad, float residual_scale,
+                                      moe_tensor_t* dx, moe_tensor_t* dweight, void* workspace,
+                                      size_t workspace_bytes, moe_stream_t stream) {
+  if (!x || !rstd || !dx || !norm_shape_ok(dout, 0.0f)) return MOE_ERR_INVALID_ARG;
+  NormBeforeBackward g;
+  g.T = dout->sizes[0];
+  g.H = static_cast<int>(dout->sizes[1]);
+  g.alpha = residual_scale;
+  MOE_TRY(rows_of(dout, g.T, g.H, false, &g.dout));
+  MOE_TRY(rows_of(x, g.T, g.H, false, &g.x));
+  if (residual_grad) MOE_TRY(rows_of(residual_grad, g.T, g.H, false, &g.dres));
+  if (residual_scale == 0.0f) g.dres = RowView();
+  MOE_TRY(rows_of(dx, g.T, g.H, true, &g.dx));
+  MOE_TRY(vector_of(weight, g.H, false, &g.w));
+  ColumnSum c = {};
+  MOE_TRY(vector_of(dweight, g.H, true, &c.dw));
+  float* r = nullptr;
+  MOE_TRY(rstd_of(rstd, g.T, false, &r, &g.rstd_s));
+  g.rstd = r;
+  if (dweight) {
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < moe_norm_backward_workspace_bytes(g.T, g.H)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  if (g.T == 0 && !dweight) return MOE_OK;
+  int sms = 0;
+  MOE_TRY(api_device(&sms, nullptr));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  g.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  int launches = 0;
+  if (g.T > 0) {
+    const bool wide = g.H % 8 == 0 && wide_ok(g.dout) && wide_ok(g.x) && wide_ok(g.dres) && wide_ok(g.dx) &&
+                      wide_ok(g.w);
+    const cudaError_t rc = launch_norm_before_backward(g, wide, sms, st);
+    if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_before_backward");
+    ++launches;
+  }
+  if (dweight) {
+    c.rows = static_cast<int>(norm_backward_rows(g.T, g.H, sms));
+    c.H = g.H;
+    c.part = g.part;
+    const cudaError_t rc = launch_column_sum(c, st);
+    if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_before_backward column sums");
+    ++launches;
+  }
+  api_set_launches(launches);
+  return MOE_OK;
+}
+
+moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_t* y,
+                                     const moe_tensor_t* rstd, const moe_tensor_t* weight,
+                                     const moe_tensor_t* gate, int32_t gate_act, int32_t normalize,
+                                     moe_tensor_t* dy, moe_tensor_t* dweight, moe_tensor_t* dgate,
+                                     void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (!y || !dy || !norm_shape_ok(dout, 0.0f) || (normalize != 0 && normalize != 1) ||
+      (normalize == 1 && !rstd) || (dgate && !gate))
+    return MOE_ERR_INVALID_ARG;
+  NormAfterBackward g;
+  g.T = dout->sizes[0];
+  g.H = static_cast<int>(dout->sizes[1]);
+  g.normalize = normalize;
+  g.act = gate_act;
+  MOE_TRY(rows_of(dout, g.T, g.H, false, &g.dout));
+  MOE_TRY(rows_of(y, g.T, g.H, false, &g.y));
+  MOE_TRY(rows_of(dy, g.T, g.H, true, &g.dy));
+  MOE_TRY(vector_of(weight, g.H, false, &g.w));
+  MOE_TRY(gate_of(gate, g.T, g.H, gate_act, &g.gate, &g.gate_mode));
+  ColumnSum c = {};
+  MOE_TRY(vector_of(dweight, g.H, true, &c.dw));
+  if (dgate) {
+    if (dgate->ndim != 2) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(rows_of(dgate, gate->sizes[0], gate->sizes[1], true, &g.dgate));
+  }
+  float* r = nullptr;
+  MOE_TRY(rstd_of(rstd, g.T, false, &r, &g.rstd_s));
+  g.rstd = r;
+  const bool gate_sum = dgate && (g.gate_mode == kGateChannel || g.gate_mode == kGateOne);
+  if (dweight || gate_sum) {
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < moe_norm_backward_workspace_bytes(g.T, g.H)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  if (g.T == 0 && !dweight && !gate_sum) return MOE_OK;
+  int sms = 0;
+  MOE_TRY(api_device(&sms, nullptr));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const size_t half = moe_norm_backward_workspace_bytes(g.T, g.H) / 2;
+  g.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  g.part_gate = gate_sum ? reinterpret_cast<float*>(static_cast<char*>(workspace) + half) : nullptr;
+  int launches = 0;
+  if (g.T > 0) {
+    const bool gate_rows = g.gate_mode == kGateFull || g.gate_mode == kGateChannel;
+    const bool wide = g.H % 8 == 0 && wide_ok(g.dout) && wide_ok(g.y) && wide_ok(g.dy) && wide_ok(g.w) &&
+                      (!gate_rows || wide_ok(g.gate)) && (g.gate_mode != kGateFull || wide_ok(g.dgate));
+    const cudaError_t rc = launch_norm_after_backward(g, wide, sms, st);
+    if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_after_backward");
+    ++launches;
+  }
+  if (dweight || gate_sum) {
+    c.rows = static_cast<int>(norm_backward_rows(g.T, g.H, sms));
+    c.H = g.H;
+    c.act = gate_act;
+    c.gate_mode = g.gate_mode;
+    c.part = g.part;
+    c.part_gate = g.part_gate;
+    c.dgate = g.dgate;
+    c.gate = g.gate;
+    c.w = g.w;
+    const cudaError_t rc = launch_column_sum(c, st);
+    if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_after_backward column sums");
+    ++launches;
+  }
+  api_set_launches(launches);
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,95 @@
+// Declarations of the operators around the expert forward (norms, the whole layer for a few
+// tokens, the 4-bit linear layer), shared by their entry points and kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe.h"
+#include "moe_common.cuh"
+
+namespace moe {
+
+// ---- from the host runtime (moe_api.cu) --------------------------------------
+
+// The current device: SM count and error counters; an error where it is not an sm_100 GPU.
+moe_status_t api_device(int* num_sms, DeviceErrors** err);
+// Records the CUDA error text of the calling thread and returns MOE_ERR_CUDA.
+moe_status_t api_cuda_fail(cudaError_t rc, const char* where);
+// A cached rank-2/3 K-major tensor map (dims[0] contiguous, strides in bytes).
+moe_status_t api_make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base,
+                          const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                          CUtensorMapSwizzle swz);
+void api_set_launches(int32_t n);
+
+// ---- norms (moe_norm.cu) -----------------------------------------------------
+
+constexpr int kNormMaxSms = 160;      // the gradient's workspace size is for at most this many SMs
+constexpr int64_t kNormMaxH = 16384;  // 1024 threads x 2 slots x 8 elements
+
+// Rows of bf16 or fp32 elements; strides in elements (s0 = 0: the same row for every token).
+struct RowView {
+  const void* data = nullptr;
+  int64_t s0 = 0, s1 = 0;
+  int32_t dtype = 0;
+};
+
+enum { kGateNone = 0, kGateFull = 1, kGateChannel = 2, kGateToken = 3, kGateOne = 4 };
+
+struct NormBefore {
+  int64_t T;
+  int H;
+  float eps;
+  RowView x, w, out;
+  float* rstd;
+  int64_t rstd_s;
+};
+struct NormAfter {
+  int64_t T;
+  int H;
+  float eps, alpha;
+  int normalize, act, gate_one_col;
+  RowView y, x, w, gate, out, wn, nxt;
+  float* rstd;
+  int64_t rstd_s;
+  float* next_rstd;
+  int64_t next_rstd_s;
+};
+struct NormBeforeBackward {
+  int64_t T;
+  int H;
+  float alpha;
+  RowView dout, x, w, dres, dx;
+  const float* rstd;
+  int64_t rstd_s;
+  float* part;  // [blocks, H] column sums, or null
+};
+struct NormAfterBackward {
+  int64_t T;
+  int H;
+  int normalize, act, gate_mode;
+  RowView dout, y, w, gate, dy, dgate;
+  const float* rstd;
+  int64_t rstd_s;
+  float* part;       // [blocks, H], or null
+  float* part_gate;  // per-channel gate [blocks, H], one gate [blocks], or null
+};
+struct ColumnSum {
+  int rows, H;
+  int act, gate_mode;
+  const float* part;
+  const float* part_gate;
+  RowView dw, dgate, gate, w;
+};
+
+// Blocks (= rows of partial column sums) of the gradient kernels.
+int64_t norm_backward_rows(int64_t T, int64_t H, int num_sms);
+// wide: every row tensor allows 16-byte accesses (see moe_norm.cu)
+cudaError_t launch_norm_before(const NormBefore& g, bool wide, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_after(const NormAfter& g, bool wide, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_before_backward(const NormBeforeBackward& g, bool wide, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_after_backward(const NormAfterBackward& g, bool wide, int num_sms, cudaStream_t st);
+cudaError_t launch_column_sum(const ColumnSum& g, cudaStream_t st);
+
+}  // namespace moe
