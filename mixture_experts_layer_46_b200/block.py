@@ -20,44 +20,55 @@ GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
 _DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.int32: MOE_I32, torch.int64: MOE_I64}
 # moe_tensor_t: data, dtype, ndim, sizes[4], strides[4], scale, scale_strides[4]
 _TENSOR = struct.Struct("=Qii4q4qQ4q").pack
-_PAD = (0, 0, 0, 0)
 
 
 def _desc(t: torch.Tensor | None):
     """The bytes of a moe_tensor_t (None stays NULL); unknown dtypes are rejected by the library."""
     if t is None:
         return None
-    n = t.dim()
+    n, z, s = t.dim(), t.shape, t.stride()
+    dt = _DT.get(t.dtype, 99)
+    if n == 2:
+        return _TENSOR(t.data_ptr(), dt, 2, z[0], z[1], 0, 0, s[0], s[1], 0, 0, 0, 0, 0, 0, 0)
+    if n == 1:
+        return _TENSOR(t.data_ptr(), dt, 1, z[0], 0, 0, 0, s[0], 0, 0, 0, 0, 0, 0, 0, 0)
     if n > 4:
         raise ValueError(f"a tensor of {n} dimensions")
-    pad = _PAD[n:]
-    return _TENSOR(t.data_ptr(), _DT.get(t.dtype, 99), n, *t.shape, *pad, *t.stride(), *pad, 0, 0, 0, 0, 0)
+    pad = (0, 0, 0, 0)[n:]
+    return _TENSOR(t.data_ptr(), dt, n, *z, *pad, *s, *pad, 0, 0, 0, 0, 0)
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 class _Call:
     """The device and stream of a call: checks that the tensors share one CUDA device, makes it
     current and, with a stream of its own, makes that the stream new tensors belong to."""
 
-    def __init__(self, stream, *tensors):
-        dev = tensors[0].device
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors on {dev} and on {t.device}")
-        if dev.type != "cuda":
-            raise ValueError(f"a tensor on {dev}: the operators run on a CUDA device only")
-        self.device, self._stack = dev, None
-        if stream is None and dev.index == torch.cuda.current_device():
-            self.stream = torch.cuda.current_stream(dev).cuda_stream
+    __slots__ = ("device", "stream", "_stack")
+
+    def __init__(self, stream, first, *others):
+        index = first.get_device()  # -1: host memory
+        for t in others:
+            if t is not None and t.get_device() != index:
+                raise ValueError(f"tensors on {first.device} and on {t.device}")
+        if index < 0:
+            raise ValueError(f"a tensor on {first.device}: the operators run on a CUDA device only")
+        self.device, self._stack = first.device, None
+        if stream is None and index == torch.cuda.current_device():
+            self.stream = _raw_stream(index)
             return
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream
+                      else torch.cuda.default_stream(self.device))
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {self.device}")
         self._stack = contextlib.ExitStack()
-        self._stack.enter_context(torch.cuda.device(dev))
+        self._stack.enter_context(torch.cuda.device(self.device))
         if stream is not None:
             self._stack.enter_context(torch.cuda.stream(stream))
-        self.stream = torch.cuda.current_stream(dev).cuda_stream
+        self.stream = _raw_stream(index)
 
     def __enter__(self):
         return self

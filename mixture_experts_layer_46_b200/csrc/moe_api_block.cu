@@ -95,6 +95,12 @@ bool norm_shape_ok(const moe_tensor_t* t, float eps) {
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// the partial column sums of a norm's gradient
+size_t norm_partial_bytes(int64_t T, int64_t H) {
+  const size_t rows = static_cast<size_t>(norm_backward_rows(T, H, kNormMaxSms));
+  return round256((rows > 0 ? rows : 1) * static_cast<size_t>(H) * sizeof(float));
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -105,18 +111,18 @@ extern "C" {
 moe_status_t moe_norm_before(const moe_tensor_t* x, const moe_tensor_t* weight, float eps,
                              moe_tensor_t* out, moe_tensor_t* rstd, moe_stream_t stream) {
   if (!out || !norm_shape_ok(x, eps)) return MOE_ERR_INVALID_ARG;
-  NormBefore g;
+  NormBefore g = {};
   g.T = x->sizes[0];
   g.H = static_cast<int>(x->sizes[1]);
   g.eps = eps;
-  MOE_TRY(rows_of(x, g.T, g.H, false, &g.x));
+  MOE_TRY(rows_of(x, g.T, g.H, false, &g.ring.in[0]));
   MOE_TRY(rows_of(out, g.T, g.H, true, &g.out));
   MOE_TRY(vector_of(weight, g.H, false, &g.w));
   MOE_TRY(rstd_of(rstd, g.T, true, &g.rstd, &g.rstd_s));
   if (g.T == 0) return MOE_OK;
   int sms = 0;
-  MOE_TRY(api_device(&sms, nullptr));
-  const bool wide = g.H % 8 == 0 && wide_ok(g.x) && wide_ok(g.out) && wide_ok(g.w);
+  MOE_TRY(api_device(&sms, &g.ring.err));
+  const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.out) && wide_ok(g.w);
   const cudaError_t rc = launch_norm_before(g, wide, sms, reinterpret_cast<cudaStream_t>(stream));
   if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_before");
   api_set_launches(1);
@@ -129,30 +135,30 @@ moe_status_t moe_norm_after(const moe_tensor_t* y, const moe_tensor_t* residual,
                             moe_tensor_t* rstd, const moe_tensor_t* next_weight,
                             moe_tensor_t* next_out, moe_tensor_t* next_rstd, moe_stream_t stream) {
   if (!out || !norm_shape_ok(y, eps) || (normalize != 0 && normalize != 1)) return MOE_ERR_INVALID_ARG;
-  NormAfter g;
+  NormAfter g = {};
   g.T = y->sizes[0];
   g.H = static_cast<int>(y->sizes[1]);
   g.eps = eps;
   g.alpha = residual_scale;
   g.normalize = normalize;
   g.act = gate_act;
-  MOE_TRY(rows_of(y, g.T, g.H, false, &g.y));
-  if (residual) MOE_TRY(rows_of(residual, g.T, g.H, false, &g.x));
-  if (residual_scale == 0.0f) g.x = RowView();
+  MOE_TRY(rows_of(y, g.T, g.H, false, &g.ring.in[0]));
+  if (residual) MOE_TRY(rows_of(residual, g.T, g.H, false, &g.ring.in[1]));
+  if (residual_scale == 0.0f) g.ring.in[1] = RowView();
   MOE_TRY(rows_of(out, g.T, g.H, true, &g.out));
   MOE_TRY(vector_of(weight, g.H, false, &g.w));
-  int mode = kGateNone;
-  MOE_TRY(gate_of(gate, g.T, g.H, gate_act, &g.gate, &mode));
-  g.gate_one_col = mode == kGateToken || mode == kGateOne;
+  MOE_TRY(gate_of(gate, g.T, g.H, gate_act, &g.gate, &g.gate_mode));
+  if (g.gate_mode == kGateFull) g.ring.in[2] = g.gate;
   MOE_TRY(rstd_of(rstd, g.T, true, &g.rstd, &g.rstd_s));
   MOE_TRY(vector_of(next_weight, g.H, false, &g.wn));
   if (next_out) MOE_TRY(rows_of(next_out, g.T, g.H, true, &g.nxt));
   MOE_TRY(rstd_of(next_rstd, g.T, true, &g.next_rstd, &g.next_rstd_s));
   if (g.T == 0) return MOE_OK;
   int sms = 0;
-  MOE_TRY(api_device(&sms, nullptr));
-  const bool wide = g.H % 8 == 0 && wide_ok(g.y) && wide_ok(g.x) && wide_ok(g.out) && wide_ok(g.w) &&
-                    (g.gate_one_col || wide_ok(g.gate)) && (!next_out || (wide_ok(g.wn) && wide_ok(g.nxt)));
+  MOE_TRY(api_device(&sms, &g.ring.err));
+  const bool gate_rows = g.gate_mode == kGateFull || g.gate_mode == kGateChannel;
+  const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.ring.in[1]) && wide_ok(g.out) &&
+                    wide_ok(g.w) && (!gate_rows || wide_ok(g.gate)) && (!next_out || (wide_ok(g.wn) && wide_ok(g.nxt)));
   const cudaError_t rc = launch_norm_after(g, wide, sms, reinterpret_cast<cudaStream_t>(stream));
   if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_after");
   api_set_launches(1);
@@ -162,7 +168,7 @@ moe_status_t moe_norm_after(const moe_tensor_t* y, const moe_tensor_t* residual,
 size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t H) {
   if (T < 0 || H < 1 || H > kNormMaxH) return 0;
   const size_t rows = static_cast<size_t>(norm_backward_rows(T, H, kNormMaxSms));
-  return 2 * round256((rows > 0 ? rows : 1) * static_cast<size_t>(H) * sizeof(float));
+  return norm_partial_bytes(T, H) + round256((rows > 0 ? rows : 1) * sizeof(float));
 }
 
 moe_status_t moe_norm_before_backward(const moe_tensor_t* dout, const moe_tensor_t* x,
@@ -171,14 +177,14 @@ moe_status_t moe_norm_before_backward(const moe_tensor_t* dout, const moe_tensor
                                       moe_tensor_t* dx, moe_tensor_t* dweight, void* workspace,
                                       size_t workspace_bytes, moe_stream_t stream) {
   if (!x || !rstd || !dx || !norm_shape_ok(dout, 0.0f)) return MOE_ERR_INVALID_ARG;
-  NormBeforeBackward g;
+  NormBeforeBackward g = {};
   g.T = dout->sizes[0];
   g.H = static_cast<int>(dout->sizes[1]);
   g.alpha = residual_scale;
-  MOE_TRY(rows_of(dout, g.T, g.H, false, &g.dout));
-  MOE_TRY(rows_of(x, g.T, g.H, false, &g.x));
-  if (residual_grad) MOE_TRY(rows_of(residual_grad, g.T, g.H, false, &g.dres));
-  if (residual_scale == 0.0f) g.dres = RowView();
+  MOE_TRY(rows_of(dout, g.T, g.H, false, &g.ring.in[0]));
+  MOE_TRY(rows_of(x, g.T, g.H, false, &g.ring.in[1]));
+  if (residual_grad) MOE_TRY(rows_of(residual_grad, g.T, g.H, false, &g.ring.in[2]));
+  if (residual_scale == 0.0f) g.ring.in[2] = RowView();
   MOE_TRY(rows_of(dx, g.T, g.H, true, &g.dx));
   MOE_TRY(vector_of(weight, g.H, false, &g.w));
   ColumnSum c = {};
@@ -192,13 +198,13 @@ moe_status_t moe_norm_before_backward(const moe_tensor_t* dout, const moe_tensor
   }
   if (g.T == 0 && !dweight) return MOE_OK;
   int sms = 0;
-  MOE_TRY(api_device(&sms, nullptr));
+  MOE_TRY(api_device(&sms, &g.ring.err));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   g.part = dweight ? static_cast<float*>(workspace) : nullptr;
   int launches = 0;
   if (g.T > 0) {
-    const bool wide = g.H % 8 == 0 && wide_ok(g.dout) && wide_ok(g.x) && wide_ok(g.dres) && wide_ok(g.dx) &&
-                      wide_ok(g.w);
+    const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.ring.in[1]) &&
+                      wide_ok(g.ring.in[2]) && wide_ok(g.dx) && wide_ok(g.w);
     const cudaError_t rc = launch_norm_before_backward(g, wide, sms, st);
     if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_before_backward");
     ++launches;
@@ -223,16 +229,17 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
   if (!y || !dy || !norm_shape_ok(dout, 0.0f) || (normalize != 0 && normalize != 1) ||
       (normalize == 1 && !rstd) || (dgate && !gate))
     return MOE_ERR_INVALID_ARG;
-  NormAfterBackward g;
+  NormAfterBackward g = {};
   g.T = dout->sizes[0];
   g.H = static_cast<int>(dout->sizes[1]);
   g.normalize = normalize;
   g.act = gate_act;
-  MOE_TRY(rows_of(dout, g.T, g.H, false, &g.dout));
-  MOE_TRY(rows_of(y, g.T, g.H, false, &g.y));
+  MOE_TRY(rows_of(dout, g.T, g.H, false, &g.ring.in[0]));
+  MOE_TRY(rows_of(y, g.T, g.H, false, &g.ring.in[1]));
   MOE_TRY(rows_of(dy, g.T, g.H, true, &g.dy));
   MOE_TRY(vector_of(weight, g.H, false, &g.w));
   MOE_TRY(gate_of(gate, g.T, g.H, gate_act, &g.gate, &g.gate_mode));
+  if (g.gate_mode == kGateFull) g.ring.in[2] = g.gate;
   ColumnSum c = {};
   MOE_TRY(vector_of(dweight, g.H, true, &c.dw));
   if (dgate) {
@@ -249,15 +256,18 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
   }
   if (g.T == 0 && !dweight && !gate_sum) return MOE_OK;
   int sms = 0;
-  MOE_TRY(api_device(&sms, nullptr));
+  MOE_TRY(api_device(&sms, &g.ring.err));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const size_t half = moe_norm_backward_workspace_bytes(g.T, g.H) / 2;
-  g.part = dweight ? static_cast<float*>(workspace) : nullptr;
-  g.part_gate = gate_sum ? reinterpret_cast<float*>(static_cast<char*>(workspace) + half) : nullptr;
+  // [partial rows][one gate's partials]; a per-channel gate's gradient comes from dweight's sums
+  const size_t rows_bytes = norm_partial_bytes(g.T, g.H);
+  g.part = dweight || (gate_sum && g.gate_mode == kGateChannel) ? static_cast<float*>(workspace) : nullptr;
+  g.part_gate = gate_sum && g.gate_mode == kGateOne
+                    ? reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes)
+                    : nullptr;
   int launches = 0;
   if (g.T > 0) {
     const bool gate_rows = g.gate_mode == kGateFull || g.gate_mode == kGateChannel;
-    const bool wide = g.H % 8 == 0 && wide_ok(g.dout) && wide_ok(g.y) && wide_ok(g.dy) && wide_ok(g.w) &&
+    const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.ring.in[1]) && wide_ok(g.dy) && wide_ok(g.w) &&
                       (!gate_rows || wide_ok(g.gate)) && (g.gate_mode != kGateFull || wide_ok(g.dgate));
     const cudaError_t rc = launch_norm_after_backward(g, wide, sms, st);
     if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_after_backward");

@@ -37,59 +37,72 @@ struct RowView {
 
 enum { kGateNone = 0, kGateFull = 1, kGateChannel = 2, kGateToken = 3, kGateOne = 4 };
 
+// A kernel's row inputs, and their ring in shared memory (stages of one row of each).
+struct RowRing {
+  RowView in[3];
+  uint32_t off[3], bytes[3];
+  uint32_t stage_bytes;
+  int stages;
+  DeviceErrors* err;
+};
+
 struct NormBefore {
+  RowRing ring;  // x
   int64_t T;
   int H;
   float eps;
-  RowView x, w, out;
+  RowView w, out;
   float* rstd;
   int64_t rstd_s;
 };
 struct NormAfter {
+  RowRing ring;  // y, the residual (or none), a gate [T, H] (or none)
   int64_t T;
   int H;
   float eps, alpha;
-  int normalize, act, gate_one_col;
-  RowView y, x, w, gate, out, wn, nxt;
+  int normalize, act, gate_mode;
+  RowView w, gate, out, wn, nxt;
   float* rstd;
   int64_t rstd_s;
   float* next_rstd;
   int64_t next_rstd_s;
 };
 struct NormBeforeBackward {
+  RowRing ring;  // dout, x, the residual's gradient (or none)
   int64_t T;
   int H;
   float alpha;
-  RowView dout, x, w, dres, dx;
+  RowView w, dx;
   const float* rstd;
   int64_t rstd_s;
   float* part;  // [blocks, H] column sums, or null
 };
 struct NormAfterBackward {
+  RowRing ring;  // dout, y, a gate [T, H] (or none)
   int64_t T;
   int H;
   int normalize, act, gate_mode;
-  RowView dout, y, w, gate, dy, dgate;
+  RowView w, gate, dy, dgate;
   const float* rstd;
   int64_t rstd_s;
-  float* part;       // [blocks, H], or null
-  float* part_gate;  // per-channel gate [blocks, H], one gate [blocks], or null
+  float* part;       // [blocks, H] column sums, or null
+  float* part_gate;  // one gate in all: [blocks], or null
 };
 struct ColumnSum {
   int rows, H;
   int act, gate_mode;
-  const float* part;
-  const float* part_gate;
+  const float* part;       // [rows, H]
+  const float* part_gate;  // [rows], or null
   RowView dw, dgate, gate, w;
 };
 
 // Blocks (= rows of partial column sums) of the gradient kernels.
 int64_t norm_backward_rows(int64_t T, int64_t H, int num_sms);
 // wide: every row tensor allows 16-byte accesses (see moe_norm.cu)
-cudaError_t launch_norm_before(const NormBefore& g, bool wide, int num_sms, cudaStream_t st);
-cudaError_t launch_norm_after(const NormAfter& g, bool wide, int num_sms, cudaStream_t st);
-cudaError_t launch_norm_before_backward(const NormBeforeBackward& g, bool wide, int num_sms, cudaStream_t st);
-cudaError_t launch_norm_after_backward(const NormAfterBackward& g, bool wide, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_before(NormBefore g, bool wide, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_after(NormAfter g, bool wide, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_before_backward(NormBeforeBackward g, bool wide, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_after_backward(NormAfterBackward g, bool wide, int num_sms, cudaStream_t st);
 cudaError_t launch_column_sum(const ColumnSum& g, cudaStream_t st);
 
 }  // namespace moe

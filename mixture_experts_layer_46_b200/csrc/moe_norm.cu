@@ -15,10 +15,13 @@
 // block writes one fp32 partial row, and a second launch adds the partial rows in a fixed
 // order (no atomics: the same inputs give the same bits).
 //
-// Two element layouts share the code: kWide reads 8 neighbours a thread with 16-byte loads
-// (inner stride 1, 16-byte aligned rows, H a multiple of 8); otherwise a thread takes every
-// blockDim-th element through the strides, which keeps a warp's accesses together.
+// Three ways to read share the code.  With inner stride 1, 16-byte aligned rows and H a
+// multiple of 8 a thread takes 8 neighbours at a time: straight from memory where a block has
+// one row, from a ring of rows in shared memory where it walks over several.  Otherwise it takes
+// every blockDim-th element through the strides, which keeps a warp's accesses together.
 // Arithmetic is fp32 throughout; each output is rounded once, to its own type.
+#include <atomic>
+
 #include "../../include/moe.h"
 #include "moe_block.h"
 #include "moe_internal.h"
@@ -30,65 +33,101 @@ struct Vec8 {
   float v[8];
 };
 
+// How a kernel reads its row tensors: through the strides, 16 bytes a load, or from the ring.
+enum { kStrided = 0, kWide = 1, kRing = 2 };
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // Eight elements of one row: element i of slot v is column (tid + v * threads) * 8 + i (wide)
 // or tid + (v * 8 + i) * threads.  Columns past H read as zero.
-template <bool kWide>
+template <bool kWideCols>
 __device__ __forceinline__ int col_of(int slot, int i) {
-  return kWide ? (static_cast<int>(threadIdx.x) + slot * static_cast<int>(blockDim.x)) * 8 + i
-               : static_cast<int>(threadIdx.x) + (slot * 8 + i) * static_cast<int>(blockDim.x);
+  return kWideCols ? (static_cast<int>(threadIdx.x) + slot * static_cast<int>(blockDim.x)) * 8 + i
+                   : static_cast<int>(threadIdx.x) + (slot * 8 + i) * static_cast<int>(blockDim.x);
 }
 
-template <bool kWide>
-__device__ __forceinline__ void load8(const RowView& t, int64_t row, int slot, int H, Vec8& o) {
-  const int64_t base = row * t.s0;
-  if (kWide) {
-    const int c = col_of<true>(slot, 0);
-    if (c >= H) {
+// Eight elements as they were read.  Loads and conversions are apart: a conversion next to its
+// load, under the branch on the type, would make every load wait for the one before.
+struct Raw8 {
+  uint32_t w[8];
+};
+
+// eight neighbours at element c of a row that starts at `row` (16-byte aligned)
+__device__ __forceinline__ void read8(const void* row, int c, int32_t dtype, Raw8& o) {
+  if (dtype == MOE_F32) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + c);
+    const uint4 a = p[0], b = p[1];
+    o.w[0] = a.x; o.w[1] = a.y; o.w[2] = a.z; o.w[3] = a.w;
+    o.w[4] = b.x; o.w[5] = b.y; o.w[6] = b.z; o.w[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c);
+    o.w[0] = a.x; o.w[1] = a.y; o.w[2] = a.z; o.w[3] = a.w;
+  }
+}
+
+__device__ __forceinline__ const char* row_ptr(const RowView& t, int64_t row) {
+  return static_cast<const char*>(t.data) + row * t.s0 * (t.dtype == MOE_F32 ? 4 : 2);
+}
+
+__device__ __forceinline__ void zero8(Raw8& o) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o.v[i] = 0.0f;
-      return;
-    }
-    if (t.dtype == MOE_F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(t.data) + base + c);
-      const float4 a = p[0], b = p[1];
-      o.v[0] = a.x; o.v[1] = a.y; o.v[2] = a.z; o.v[3] = a.w;
-      o.v[4] = b.x; o.v[5] = b.y; o.v[6] = b.z; o.v[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(t.data) + base + c);
-      o.v[0] = bf16_lo(a.x); o.v[1] = bf16_hi(a.x); o.v[2] = bf16_lo(a.y); o.v[3] = bf16_hi(a.y);
-      o.v[4] = bf16_lo(a.z); o.v[5] = bf16_hi(a.z); o.v[6] = bf16_lo(a.w); o.v[7] = bf16_hi(a.w);
+  for (int i = 0; i < 8; ++i) o.w[i] = 0u;
+}
+
+template <int kMode>
+__device__ __forceinline__ void load8(const RowView& t, int64_t row, int slot, int H, Raw8& o) {
+  const char* base = row_ptr(t, row);
+  zero8(o);
+  if (kMode != kStrided) {
+    const int c = col_of<true>(slot, 0);
+    if (c < H) read8(base, c, t.dtype, o);
+  } else if (t.dtype == MOE_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = col_of<false>(slot, i);
+      if (c < H) o.w[i] = reinterpret_cast<const uint32_t*>(base)[c * t.s1];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = col_of<false>(slot, i);
-      float f = 0.0f;
-      if (c < H) {
-        const int64_t off = base + c * t.s1;
-        f = t.dtype == MOE_F32 ? static_cast<const float*>(t.data)[off]
-                               : bf16_lo(static_cast<const uint16_t*>(t.data)[off]);
-      }
-      o.v[i] = f;
+      if (c < H) o.w[i] = reinterpret_cast<const uint16_t*>(base)[c * t.s1];
     }
   }
 }
 
-template <bool kWide>
+template <int kMode>
+__device__ __forceinline__ Vec8 unpack8(const Raw8& r, int32_t dtype) {
+  Vec8 o;
+  if (dtype == MOE_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.v[i] = __uint_as_float(r.w[i]);
+  } else if (kMode != kStrided) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o.v[2 * i] = bf16_lo(r.w[i]);
+      o.v[2 * i + 1] = bf16_hi(r.w[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.v[i] = bf16_lo(r.w[i]);
+  }
+  return o;
+}
+
+template <int kMode>
 __device__ __forceinline__ void store8(const RowView& t, int64_t row, int slot, int H, const Vec8& o) {
-  const int64_t base = row * t.s0;
-  void* data = const_cast<void*>(t.data);
-  if (kWide) {
+  char* base = const_cast<char*>(row_ptr(t, row));
+  if (kMode != kStrided) {
     const int c = col_of<true>(slot, 0);
     if (c >= H) return;
     if (t.dtype == MOE_F32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(data) + base + c);
+      float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + c);
       p[0] = make_float4(o.v[0], o.v[1], o.v[2], o.v[3]);
       p[1] = make_float4(o.v[4], o.v[5], o.v[6], o.v[7]);
     } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(data) + base + c) =
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + c) =
           make_uint4(pack_bf16x2(o.v[0], o.v[1]), pack_bf16x2(o.v[2], o.v[3]),
                      pack_bf16x2(o.v[4], o.v[5]), pack_bf16x2(o.v[6], o.v[7]));
     }
@@ -97,24 +136,95 @@ __device__ __forceinline__ void store8(const RowView& t, int64_t row, int slot, 
     for (int i = 0; i < 8; ++i) {
       const int c = col_of<false>(slot, i);
       if (c >= H) continue;
-      const int64_t off = base + c * t.s1;
       if (t.dtype == MOE_F32)
-        static_cast<float*>(data)[off] = o.v[i];
+        reinterpret_cast<float*>(base)[c * t.s1] = o.v[i];
       else
-        static_cast<__nv_bfloat16*>(data)[off] = __float2bfloat16_rn(o.v[i]);
+        reinterpret_cast<__nv_bfloat16*>(base)[c * t.s1] = __float2bfloat16_rn(o.v[i]);
     }
   }
 }
 
+// The ring: a block's next rows on their way into shared memory by bulk copies (one copy a
+// tensor and row, all of a stage on one mbarrier) while the current row is reduced, so that
+// memory never waits for the two barriers of a reduction.
+struct Ring {
+  const RowRing& a;
+  char* smem;
+  uint64_t* full;
+  uint32_t stage, phase;
+  bool ok;
+
+  __device__ __forceinline__ Ring(const RowRing& args, char* raw) : a(args) {
+    full = reinterpret_cast<uint64_t*>(raw);
+    smem = raw + 128;
+    stage = 0;
+    phase = 0;
+    ok = true;
+  }
+  // thread 0: the copies of row t into stage s
+  __device__ __forceinline__ void fill(int s, int64_t t) {
+    mbar_arrive_expect_tx(&full[s], a.stage_bytes);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (a.in[i].data)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                smem_u32(smem + s * a.stage_bytes + a.off[i])),
+            "l"(row_ptr(a.in[i], t)), "r"(a.bytes[i]), "r"(smem_u32(&full[s]))
+            : "memory");
+  }
+  __device__ __forceinline__ void start(int64_t T) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+      fence_barrier_init();
+      fence_proxy_async_smem();
+      for (int s = 0; s < a.stages; ++s) {
+        const int64_t t = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+        if (t < T) fill(s, t);
+      }
+    }
+    __syncthreads();
+  }
+  // waits (bounded) for the current stage
+  __device__ __forceinline__ void wait() {
+    if (ok && !mbar_wait(&full[stage], phase, threadIdx.x == 0 ? a.err : nullptr)) ok = false;
+  }
+  __device__ __forceinline__ void read(int i, int slot, int H, Raw8& o) const {
+    const int c = col_of<true>(slot, 0);
+    zero8(o);
+    if (c < H) read8(smem + stage * a.stage_bytes + a.off[i], c, a.in[i].dtype, o);
+  }
+  // every thread has read its part of row t: the stage takes the row `stages` rounds on
+  __device__ __forceinline__ void next(int64_t t, int64_t T) {
+    __syncthreads();
+    const int64_t n = t + static_cast<int64_t>(a.stages) * gridDim.x;
+    if (threadIdx.x == 0 && n < T && ok) fill(stage, n);
+    if (++stage == static_cast<uint32_t>(a.stages)) { stage = 0; phase ^= 1u; }
+  }
+};
+
+// row tensor i of the kernel: from the ring, or from memory
+template <int kMode>
+__device__ __forceinline__ void input8(const Ring& ring, int i, int64_t row, int slot, int H, Raw8& o) {
+  if (kMode == kRing)
+    ring.read(i, slot, H, o);
+  else
+    load8<kMode>(ring.a.in[i], row, slot, H, o);
+}
+
 // a weight vector (or ones): element c at data[c * s1]
-template <bool kWide>
-__device__ __forceinline__ void load_weight(const RowView& t, int slot, int H, Vec8& o) {
+template <int kMode>
+__device__ __forceinline__ Vec8 load_weight(const RowView& t, int slot, int H) {
+  Vec8 o;
   if (t.data) {
-    load8<kWide>(t, 0, slot, H, o);
+    Raw8 r;
+    load8<kMode>(t, 0, slot, H, r);
+    o = unpack8<kMode>(r, t.dtype);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) o.v[i] = 1.0f;
   }
+  return o;
 }
 
 __device__ __forceinline__ float scalar_at(const RowView& t, int64_t off) {
@@ -142,6 +252,17 @@ __device__ __forceinline__ float gate_slope(float g, int act) {
   return 1.0f;
 }
 
+// the same on eight values, the choice of function outside the loop
+__device__ __forceinline__ void gate_values(Vec8& g, int act) {
+  if (act == MOE_GATE_NONE) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g.v[i] = gate_value(g.v[i], act);
+}
+__device__ __forceinline__ void gate_slopes(Vec8& g, int act) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g.v[i] = gate_slope(g.v[i], act);
+}
+
 // Sum of v over the block; every thread gets it.  One barrier a call: two scratch rows are
 // used in turn, and a row is written again only after the other one's barrier.
 __device__ __forceinline__ float block_sum(float v, float (*scratch)[32], int& turn) {
@@ -163,52 +284,100 @@ __device__ __forceinline__ float inv_root(float sum, int H, float eps) {
   return 1.0f / sqrtf(sum / static_cast<float>(H) + eps);
 }
 
+// Threads of resident blocks on an SM: 80 and 128 registers a thread, what the kernels need
+// without spilling up to 4096 elements a row (the ring, not the number of warps, keeps memory busy).
+constexpr int kRingThreads = 768, kDirectThreads = 512, kBackwardThreads = 512;
+constexpr int min_blocks(int threads_per_sm, int max_threads) {
+  return threads_per_sm / max_threads < 1 ? 1 : threads_per_sm / max_threads;
+}
+constexpr int forward_threads(bool ring) { return ring ? kRingThreads : kDirectThreads; }
+
 // ---------------------------------------------------------------- forward
 
-template <int kVec, bool kWide, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) norm_before_kernel(const NormBefore g) {
+template <int kVec, int kMode, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(kMode == kRing), kMaxThreads))
+    norm_before_kernel(const NormBefore g) {
+  extern __shared__ __align__(128) char smem[];
   __shared__ float scratch[2][32];
   pdl_wait();
   pdl_launch_dependents();
   int turn = 0;
+  Ring ring(g.ring, smem);
+  if (kMode == kRing) ring.start(g.T);
+  Vec8 w[kVec];
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) w[v] = load_weight<kMode>(g.w, v, g.H);
   for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
+    if (kMode == kRing) ring.wait();
+    Raw8 raw[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) input8<kMode>(ring, 0, t, v, g.H, raw[v]);
+    if (kMode == kRing) ring.next(t, g.T);
     Vec8 x[kVec];
     float ss = 0.0f;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) load8<kWide>(g.x, t, v, g.H, x[v]);
-#pragma unroll
-    for (int v = 0; v < kVec; ++v)
+    for (int v = 0; v < kVec; ++v) {
+      x[v] = unpack8<kMode>(raw[v], g.ring.in[0].dtype);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss += x[v].v[i] * x[v].v[i];
+    }
     const float r = inv_root(block_sum(ss, scratch, turn), g.H, g.eps);
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      Vec8 w;
-      load_weight<kWide>(g.w, v, g.H, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w.v[i] *= x[v].v[i] * r;
-      store8<kWide>(g.out, t, v, g.H, w);
+      for (int i = 0; i < 8; ++i) x[v].v[i] *= r * w[v].v[i];
+      store8<kMode>(g.out, t, v, g.H, x[v]);
     }
     if (g.rstd && threadIdx.x == 0) g.rstd[t * g.rstd_s] = r;
   }
 }
 
 // One pass over (y, x, gate): out and, with a next norm, its output too.  The row of out is
-// kept in registers unrounded between the two reductions.
-template <int kVec, bool kWide, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) norm_after_kernel(const NormAfter g) {
+// kept in registers unrounded between the two reductions, the weights (a per-channel gate
+// multiplied in) for all of the block's rows.
+template <int kVec, int kMode, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(kMode == kRing), kMaxThreads))
+    norm_after_kernel(const NormAfter g) {
+  extern __shared__ __align__(128) char smem[];
   __shared__ float scratch[2][32];
   pdl_wait();
   pdl_launch_dependents();
   int turn = 0;
-  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    Vec8 o[kVec], x[kVec];
+  Ring ring(g.ring, smem);
+  if (kMode == kRing) ring.start(g.T);
+  const bool have_x = g.ring.in[1].data != nullptr;
+  const bool gate_full = g.ring.in[2].data != nullptr;
+  const bool want_next = g.nxt.data || g.next_rstd;
+  Vec8 w[kVec], wn[kVec];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) load8<kWide>(g.y, t, v, g.H, o[v]);
-    if (g.x.data) {
+  for (int v = 0; v < kVec; ++v) {
+    w[v] = load_weight<kMode>(g.w, v, g.H);
+    if (g.nxt.data) wn[v] = load_weight<kMode>(g.wn, v, g.H);
+    if (g.gate_mode == kGateChannel) {
+      Vec8 c = load_weight<kMode>(g.gate, v, g.H);
+      gate_values(c, g.act);
 #pragma unroll
-      for (int v = 0; v < kVec; ++v) load8<kWide>(g.x, t, v, g.H, x[v]);
+      for (int i = 0; i < 8; ++i) w[v].v[i] *= c.v[i];
     }
+  }
+  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
+    if (kMode == kRing) ring.wait();
+    Raw8 y[kVec], x[kVec], gt[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) input8<kMode>(ring, 0, t, v, g.H, y[v]);
+    if (kMode != kRing) {  // (the ring's rows wait in shared memory until they are needed)
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        if (have_x) input8<kMode>(ring, 1, t, v, g.H, x[v]);
+        if (gate_full) input8<kMode>(ring, 2, t, v, g.H, gt[v]);
+      }
+    }
+    // a gate of one number a row (or one in all) is part of the row's factor
+    float f = 1.0f;
+    if (g.gate_mode == kGateToken || g.gate_mode == kGateOne) f = gate_value(scalar_at(g.gate, t * g.gate.s0), g.act);
+    Vec8 o[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) o[v] = unpack8<kMode>(y[v], g.ring.in[0].dtype);
     float r = 1.0f;
     if (g.normalize) {
       float ss = 0.0f;
@@ -219,43 +388,39 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_kernel(const NormAfter
       r = inv_root(block_sum(ss, scratch, turn), g.H, g.eps);
     }
     if (g.rstd && threadIdx.x == 0) g.rstd[t * g.rstd_s] = r;
-    // a gate of one number a row (or one in all) is part of the row's factor
-    float rowg = 1.0f;
-    if (g.gate.data && g.gate_one_col) rowg = gate_value(scalar_at(g.gate, t * g.gate.s0), g.act);
+    f *= r;
     float ss = 0.0f;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      Vec8 w;
-      load_weight<kWide>(g.w, v, g.H, w);
-      if (g.gate.data && !g.gate_one_col) {
-        Vec8 gt;
-        load8<kWide>(g.gate, t, v, g.H, gt);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w.v[i] *= gate_value(gt.v[i], g.act);
-      } else {
+      for (int i = 0; i < 8; ++i) o[v].v[i] *= f * w[v].v[i];
+      if (gate_full) {
+        if (kMode == kRing) input8<kMode>(ring, 2, t, v, g.H, gt[v]);
+        Vec8 c = unpack8<kMode>(gt[v], g.ring.in[2].dtype);
+        gate_values(c, g.act);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w.v[i] *= rowg;
+        for (int i = 0; i < 8; ++i) o[v].v[i] *= c.v[i];
       }
+      if (have_x) {
+        if (kMode == kRing) input8<kMode>(ring, 1, t, v, g.H, x[v]);
+        const Vec8 c = unpack8<kMode>(x[v], g.ring.in[1].dtype);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float z = o[v].v[i] * r * w.v[i];
-        if (g.x.data) z += g.alpha * x[v].v[i];
-        o[v].v[i] = z;
-        ss += z * z;
+        for (int i = 0; i < 8; ++i) o[v].v[i] += g.alpha * c.v[i];
       }
-      store8<kWide>(g.out, t, v, g.H, o[v]);
+      store8<kMode>(g.out, t, v, g.H, o[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += o[v].v[i] * o[v].v[i];
     }
-    if (g.nxt.data || g.next_rstd) {
+    if (kMode == kRing) ring.next(t, g.T);
+    if (want_next) {
       const float rn = inv_root(block_sum(ss, scratch, turn), g.H, g.eps);
       if (g.next_rstd && threadIdx.x == 0) g.next_rstd[t * g.next_rstd_s] = rn;
       if (g.nxt.data) {
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
-          Vec8 w;
-          load_weight<kWide>(g.wn, v, g.H, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w.v[i] *= o[v].v[i] * rn;
-          store8<kWide>(g.nxt, t, v, g.H, w);
+          for (int i = 0; i < 8; ++i) o[v].v[i] *= rn * wn[v].v[i];
+          store8<kMode>(g.nxt, t, v, g.H, o[v]);
         }
       }
     }
@@ -265,7 +430,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_kernel(const NormAfter
 // ---------------------------------------------------------------- backward
 
 // Partial column sums of this block into row blockIdx.x of part [gridDim.x, H].
-template <int kVec, bool kWide>
+template <int kVec, int kMode>
 __device__ __forceinline__ void store_partial(float* part, int H, const Vec8 (&acc)[kVec]) {
   RowView p;
   p.data = part;
@@ -273,39 +438,48 @@ __device__ __forceinline__ void store_partial(float* part, int H, const Vec8 (&a
   p.s1 = 1;
   p.dtype = MOE_F32;
 #pragma unroll
-  for (int v = 0; v < kVec; ++v) store8<kWide>(p, blockIdx.x, v, H, acc[v]);
+  for (int v = 0; v < kVec; ++v) store8<kMode>(p, blockIdx.x, v, H, acc[v]);
 }
 
-template <int kVec, bool kWide, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) norm_before_backward_kernel(const NormBeforeBackward g) {
+template <int kVec, int kMode, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMaxThreads))
+    norm_before_backward_kernel(const NormBeforeBackward g) {
+  extern __shared__ __align__(128) char smem[];
   __shared__ float scratch[2][32];
   pdl_wait();
   pdl_launch_dependents();
   int turn = 0;
-  Vec8 dw[kVec];
+  Ring ring(g.ring, smem);
+  if (kMode == kRing) ring.start(g.T);
+  const bool have_res = g.ring.in[2].data != nullptr;
+  Vec8 dw[kVec], w[kVec];
 #pragma unroll
-  for (int v = 0; v < kVec; ++v)
+  for (int v = 0; v < kVec; ++v) {
+    w[v] = load_weight<kMode>(g.w, v, g.H);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v].v[i] = 0.0f;
+  }
   for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    Vec8 p[kVec], x[kVec], d[kVec];
+    const float r = g.rstd[t * g.rstd_s];
+    if (kMode == kRing) ring.wait();
+    Raw8 rd[kVec], rx[kVec], res[kVec];
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      load8<kWide>(g.dout, t, v, g.H, p[v]);
-      load8<kWide>(g.x, t, v, g.H, x[v]);
-      if (g.dres.data) load8<kWide>(g.dres, t, v, g.H, d[v]);
+      input8<kMode>(ring, 0, t, v, g.H, rd[v]);
+      input8<kMode>(ring, 1, t, v, g.H, rx[v]);
+      if (kMode != kRing && have_res) input8<kMode>(ring, 2, t, v, g.H, res[v]);
     }
-    const float r = g.rstd[t * g.rstd_s];
+    Vec8 p[kVec], x[kVec];
     float dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      Vec8 w;
-      load_weight<kWide>(g.w, v, g.H, w);
+      p[v] = unpack8<kMode>(rd[v], g.ring.in[0].dtype);
+      x[v] = unpack8<kMode>(rx[v], g.ring.in[1].dtype);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[v].v[i] *= r;
         dw[v].v[i] += p[v].v[i] * x[v].v[i];
-        p[v].v[i] *= w.v[i];
+        p[v].v[i] *= w[v].v[i];
         dot += p[v].v[i] * x[v].v[i];
       }
     }
@@ -313,39 +487,48 @@ __global__ void __launch_bounds__(kMaxThreads) norm_before_backward_kernel(const
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float z = r * (p[v].v[i] - x[v].v[i] * c);
-        if (g.dres.data) z += g.alpha * d[v].v[i];
-        p[v].v[i] = z;
+      for (int i = 0; i < 8; ++i) p[v].v[i] = r * (p[v].v[i] - x[v].v[i] * c);
+      if (have_res) {
+        if (kMode == kRing) input8<kMode>(ring, 2, t, v, g.H, res[v]);
+        const Vec8 d = unpack8<kMode>(res[v], g.ring.in[2].dtype);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[v].v[i] += g.alpha * d.v[i];
       }
-      store8<kWide>(g.dx, t, v, g.H, p[v]);
+      store8<kMode>(g.dx, t, v, g.H, p[v]);
     }
+    if (kMode == kRing) ring.next(t, g.T);
   }
-  if (g.part) store_partial<kVec, kWide>(g.part, g.H, dw);
+  if (g.part) store_partial<kVec, kMode>(g.part, g.H, dw);
 }
 
-template <int kVec, bool kWide, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) norm_after_backward_kernel(const NormAfterBackward g) {
+template <int kVec, int kMode, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMaxThreads))
+    norm_after_backward_kernel(const NormAfterBackward g) {
+  extern __shared__ __align__(128) char smem[];
   __shared__ float scratch[2][32];
   pdl_wait();
   pdl_launch_dependents();
   int turn = 0;
+  Ring ring(g.ring, smem);
+  if (kMode == kRing) ring.start(g.T);
   const bool gate_full = g.gate_mode == kGateFull;
   const bool gate_col = g.gate_mode == kGateChannel;
   const bool gate_row = g.gate_mode == kGateToken || g.gate_mode == kGateOne;
-  Vec8 dw[kVec], dc[kVec];
-  float dall = 0.0f;  // one gate in all: this block's rows
+  Vec8 dw[kVec], w[kVec];  // w: the weight, a per-channel gate's value multiplied in
+  float dall = 0.0f;       // one gate in all: this block's rows
 #pragma unroll
-  for (int v = 0; v < kVec; ++v)
+  for (int v = 0; v < kVec; ++v) {
+    w[v] = load_weight<kMode>(g.w, v, g.H);
+    if (gate_col) {
+      Vec8 c = load_weight<kMode>(g.gate, v, g.H);
+      gate_values(c, g.act);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[v].v[i] = dc[v].v[i] = 0.0f;
-  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    Vec8 d[kVec], y[kVec];
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      load8<kWide>(g.dout, t, v, g.H, d[v]);
-      load8<kWide>(g.y, t, v, g.H, y[v]);
+      for (int i = 0; i < 8; ++i) w[v].v[i] *= c.v[i];
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[v].v[i] = 0.0f;
+  }
+  for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
     const float r = g.normalize ? g.rstd[t * g.rstd_s] : 1.0f;
     float rowv = 1.0f, rowslope = 1.0f;
     if (gate_row) {
@@ -353,33 +536,48 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_backward_kernel(const 
       rowv = gate_value(raw, g.act);
       rowslope = gate_slope(raw, g.act);
     }
+    if (kMode == kRing) ring.wait();
+    Raw8 rd[kVec], ry[kVec], rg[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      input8<kMode>(ring, 0, t, v, g.H, rd[v]);
+      input8<kMode>(ring, 1, t, v, g.H, ry[v]);
+      if (kMode != kRing && gate_full) input8<kMode>(ring, 2, t, v, g.H, rg[v]);
+    }
+    Vec8 d[kVec], y[kVec];
     float dot = 0.0f, gsum = 0.0f;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      Vec8 w, gt;
-      load_weight<kWide>(g.w, v, g.H, w);
-      if (gate_full || gate_col) load8<kWide>(g.gate, t, v, g.H, gt);
+      d[v] = unpack8<kMode>(rd[v], g.ring.in[0].dtype);
+      y[v] = unpack8<kMode>(ry[v], g.ring.in[1].dtype);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[v].v[i] *= r;
+      if (gate_full) {
+        if (kMode == kRing) input8<kMode>(ring, 2, t, v, g.H, rg[v]);
+        Vec8 c = unpack8<kMode>(rg[v], g.ring.in[2].dtype);
+        if (g.dgate.data) {
+          Vec8 e = c;
+          gate_slopes(e, g.act);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) e.v[i] *= d[v].v[i] * y[v].v[i] * w[v].v[i];
+          store8<kMode>(g.dgate, t, v, g.H, e);
+        }
+        gate_values(c, g.act);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[v].v[i] *= c.v[i];
+      }
+      // the column sum of dout yh: times a(g) it is dw, and for a gate that is the same in every
+      // row of the column times w a'(g) it is dg, so one sum serves both there
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float yh = y[v].v[i] * r;
-        const float dy0 = d[v].v[i] * yh;  // dout yh
-        float a = rowv;
-        if (gate_full || gate_col) {
-          a = gate_value(gt.v[i], g.act);
-          if (gate_full)
-            gt.v[i] = dy0 * w.v[i] * gate_slope(gt.v[i], g.act);
-          else
-            dc[v].v[i] += dy0;  // w a'(g) of a column is the same in every row: applied at the end
-        } else {
-          gsum += dy0 * w.v[i];
-        }
-        y[v].v[i] = yh;
-        dw[v].v[i] += a * dy0;
-        d[v].v[i] *= a * w.v[i];
-        dot += d[v].v[i] * yh;
+        const float e = d[v].v[i] * y[v].v[i];
+        dw[v].v[i] += rowv * e;
+        if (gate_row) gsum += e * w[v].v[i];
+        d[v].v[i] *= rowv * w[v].v[i];
+        dot += d[v].v[i] * y[v].v[i];
       }
-      if (gate_full && g.dgate.data) store8<kWide>(g.dgate, t, v, g.H, gt);
     }
+    if (kMode == kRing) ring.next(t, g.T);
     float c = 0.0f;
     if (g.normalize) c = block_sum(dot, scratch, turn) / static_cast<float>(g.H);
     if (gate_row && g.dgate.data) {
@@ -399,49 +597,52 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_backward_kernel(const 
     for (int v = 0; v < kVec; ++v) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[v].v[i] = r * (d[v].v[i] - y[v].v[i] * c);
-      store8<kWide>(g.dy, t, v, g.H, y[v]);
+      store8<kMode>(g.dy, t, v, g.H, y[v]);
     }
   }
-  if (g.part) store_partial<kVec, kWide>(g.part, g.H, dw);
-  if (g.part_gate) {
-    if (gate_col)
-      store_partial<kVec, kWide>(g.part_gate, g.H, dc);
-    else if (threadIdx.x == 0)
-      g.part_gate[blockIdx.x] = dall;
-  }
+  if (g.part) store_partial<kVec, kMode>(g.part, g.H, dw);
+  if (g.part_gate && threadIdx.x == 0) g.part_gate[blockIdx.x] = dall;
 }
 
-// out[c] = sum of the partial rows, in row order within each of 32 strips and then over the
-// strips; for a per-channel gate times w a'(g).  blockIdx.y = 0: dw, 1: the gate's sum.
+// Adds up the partial rows, in row order within each of 32 strips and then over the strips:
+// dw[c] = a(g) sum (the gate is folded into the terms unless it is per channel), and for a
+// per-channel gate dgate[c] = w a'(g) sum.  blockIdx.y = 1 sums the one-number gate's partials.
 constexpr int kStrips = 32;
+__device__ __forceinline__ void store1(const RowView& t, int64_t off, float v) {
+  if (t.dtype == MOE_F32)
+    static_cast<float*>(const_cast<void*>(t.data))[off] = v;
+  else
+    static_cast<__nv_bfloat16*>(const_cast<void*>(t.data))[off] = __float2bfloat16_rn(v);
+}
 __global__ void __launch_bounds__(32 * kStrips) column_sum_kernel(const ColumnSum g) {
   __shared__ float acc[kStrips][33];
   pdl_wait();
   pdl_launch_dependents();
-  const bool gate = blockIdx.y == 1;
-  const float* part = gate ? g.part_gate : g.part;
-  if (!part) return;
-  const RowView& out = gate ? g.dgate : g.dw;
-  const int n = gate && g.gate_mode == kGateOne ? 1 : g.H;
+  const bool one = blockIdx.y == 1;
+  const float* part = one ? g.part_gate : g.part;
+  const int n = one ? 1 : g.H;
   const int c = blockIdx.x * 32 + threadIdx.x;
+  if (one && blockIdx.x != 0) return;
   float s = 0.0f;
-  if (c < n)
+  if (c < n && part)
     for (int row = threadIdx.y; row < g.rows; row += kStrips) s += part[static_cast<int64_t>(row) * n + c];
   acc[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || c >= n) return;
   s = 0.0f;
   for (int i = 0; i < kStrips; ++i) s += acc[i][threadIdx.x];
-  if (gate) {
-    const float raw = scalar_at(g.gate, g.gate_mode == kGateOne ? 0 : c * g.gate.s1);
-    s *= gate_slope(raw, g.act);
-    if (g.gate_mode == kGateChannel && g.w.data) s *= scalar_at(g.w, c * g.w.s1);
+  if (one) {
+    store1(g.dgate, 0, s * gate_slope(scalar_at(g.gate, 0), g.act));
+    return;
   }
-  const int64_t off = c * out.s1;
-  if (out.dtype == MOE_F32)
-    static_cast<float*>(const_cast<void*>(out.data))[off] = s;
-  else
-    static_cast<__nv_bfloat16*>(const_cast<void*>(out.data))[off] = __float2bfloat16_rn(s);
+  float a = 1.0f;
+  if (g.gate_mode == kGateChannel) {
+    const float raw = scalar_at(g.gate, c * g.gate.s1);
+    a = gate_value(raw, g.act);
+    if (g.dgate.data)
+      store1(g.dgate, c * g.dgate.s1, s * gate_slope(raw, g.act) * (g.w.data ? scalar_at(g.w, c * g.w.s1) : 1.0f));
+  }
+  if (g.dw.data) store1(g.dw, c * g.dw.s1, s * a);
 }
 
 // ---------------------------------------------------------------- launch
@@ -467,44 +668,92 @@ int64_t blocks_of(int64_t T, int threads, int num_sms, int threads_per_sm) {
   return T < g ? T : g;
 }
 
-// Launches K<kVec, kWide, threads bound> for the row shape.
-#define MOE_NORM_LAUNCH(K, g, wide, s, grid, st)                                                              \
-  [&]() -> cudaError_t {                                                                                      \
-    const dim3 gr(static_cast<unsigned>(grid)), bl(static_cast<unsigned>((s).threads));                       \
-    if ((s).vec == 1) return (wide) ? launch_pdl(K<1, true, 256>, gr, bl, 0, st, g)                           \
-                                    : launch_pdl(K<1, false, 256>, gr, bl, 0, st, g);                         \
-    if ((s).threads <= 256) return (wide) ? launch_pdl(K<2, true, 256>, gr, bl, 0, st, g)                     \
-                                          : launch_pdl(K<2, false, 256>, gr, bl, 0, st, g);                   \
-    if ((s).threads <= 512) return (wide) ? launch_pdl(K<2, true, 512>, gr, bl, 0, st, g)                     \
-                                          : launch_pdl(K<2, false, 512>, gr, bl, 0, st, g);                   \
-    return (wide) ? launch_pdl(K<2, true, 1024>, gr, bl, 0, st, g)                                            \
-                  : launch_pdl(K<2, false, 1024>, gr, bl, 0, st, g);                                          \
-  }()
+// The ring of a wide call in which blocks walk over several rows: as many stages (up to 4) as
+// let `per_sm` blocks share an SM's 220 KB; none where the rows do not fit.
+int ring_of(RowRing* r, int H, int64_t T, int64_t grid, int per_sm) {
+  r->stage_bytes = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!r->in[i].data) continue;
+    r->off[i] = r->stage_bytes;
+    r->bytes[i] = static_cast<uint32_t>(H) * (r->in[i].dtype == MOE_F32 ? 4u : 2u);
+    r->stage_bytes += r->bytes[i];
+  }
+  const int64_t room = (220 << 10) / per_sm - 1024 - 128;
+  int64_t n = room / r->stage_bytes;
+  if (n > 4) n = 4;
+  const int64_t rows = (T + grid - 1) / grid;
+  if (n > rows) n = rows;
+  r->stages = static_cast<int>(n);
+  return rows > 1 && n >= 2 ? 128 + r->stages * static_cast<int>(r->stage_bytes) : 0;
+}
+
+template <auto kKernel, typename Args>
+cudaError_t launch_rows(const Args& g, int threads, int64_t grid, int smem, cudaStream_t st) {
+  if (smem > (48 << 10)) {
+    static std::atomic<unsigned long long> configured{0};  // devices whose limit is raised already
+    int dev = 0;
+    cudaError_t rc = cudaGetDevice(&dev);
+    if (rc != cudaSuccess) return rc;
+    if (dev >= 64 || !(configured.load() & (1ull << dev))) {
+      rc = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 << 10);
+      if (rc != cudaSuccess) return rc;
+      if (dev < 64) configured.fetch_or(1ull << dev);
+    }
+  }
+  return launch_pdl(kKernel, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)), smem, st, g);
+}
+
+// Launches K<slots, mode, threads bound> for a row of H elements.
+#define MOE_NORM_MODE(K, V, M, g, s, grid, smem, st)                                                  \
+  ((s).threads <= 256   ? launch_rows<K<V, M, 256>>(g, (s).threads, grid, smem, st)                   \
+   : (s).threads <= 512 ? launch_rows<K<2, M, 512>>(g, (s).threads, grid, smem, st)                   \
+                        : launch_rows<K<2, M, 1024>>(g, (s).threads, grid, smem, st))
+#define MOE_NORM_LAUNCH(K, g, wide, s, grid, smem, st)                                                \
+  ((s).vec == 1 ? (!(wide)     ? MOE_NORM_MODE(K, 1, kStrided, g, s, grid, 0, st)                     \
+                   : (smem) == 0 ? MOE_NORM_MODE(K, 1, kWide, g, s, grid, 0, st)                      \
+                                 : MOE_NORM_MODE(K, 1, kRing, g, s, grid, smem, st))                  \
+                : (!(wide)     ? MOE_NORM_MODE(K, 2, kStrided, g, s, grid, 0, st)                     \
+                   : (smem) == 0 ? MOE_NORM_MODE(K, 2, kWide, g, s, grid, 0, st)                      \
+                                 : MOE_NORM_MODE(K, 2, kRing, g, s, grid, smem, st)))
+
+template <typename Args>
+int prepare(Args* g, const Shape& s, bool wide, int threads_per_sm, int64_t grid) {
+  const int per = threads_per_sm / s.threads < 1 ? 1 : threads_per_sm / s.threads > 16 ? 16 : threads_per_sm / s.threads;
+  return wide ? ring_of(&g->ring, g->H, g->T, grid, per) : 0;
+}
 
 }  // namespace
 
 int64_t norm_backward_rows(int64_t T, int64_t H, int num_sms) {
-  return blocks_of(T, shape_of(H).threads, num_sms < kNormMaxSms ? num_sms : kNormMaxSms, 512);
+  return blocks_of(T, shape_of(H).threads, num_sms < kNormMaxSms ? num_sms : kNormMaxSms, kBackwardThreads);
 }
 
-cudaError_t launch_norm_before(const NormBefore& g, bool wide, int num_sms, cudaStream_t st) {
+cudaError_t launch_norm_before(NormBefore g, bool wide, int num_sms, cudaStream_t st) {
   const Shape s = shape_of(g.H);
-  return MOE_NORM_LAUNCH(norm_before_kernel, g, wide, s, blocks_of(g.T, s.threads, num_sms, 2048), st);
+  const int64_t grid = blocks_of(g.T, s.threads, num_sms, forward_threads(wide));
+  const int smem = prepare(&g, s, wide, forward_threads(wide), grid);
+  return MOE_NORM_LAUNCH(norm_before_kernel, g, wide, s, grid, smem, st);
 }
 
-cudaError_t launch_norm_after(const NormAfter& g, bool wide, int num_sms, cudaStream_t st) {
+cudaError_t launch_norm_after(NormAfter g, bool wide, int num_sms, cudaStream_t st) {
   const Shape s = shape_of(g.H);
-  return MOE_NORM_LAUNCH(norm_after_kernel, g, wide, s, blocks_of(g.T, s.threads, num_sms, 2048), st);
+  const int64_t grid = blocks_of(g.T, s.threads, num_sms, forward_threads(wide));
+  const int smem = prepare(&g, s, wide, forward_threads(wide), grid);
+  return MOE_NORM_LAUNCH(norm_after_kernel, g, wide, s, grid, smem, st);
 }
 
-cudaError_t launch_norm_before_backward(const NormBeforeBackward& g, bool wide, int num_sms, cudaStream_t st) {
+cudaError_t launch_norm_before_backward(NormBeforeBackward g, bool wide, int num_sms, cudaStream_t st) {
   const Shape s = shape_of(g.H);
-  return MOE_NORM_LAUNCH(norm_before_backward_kernel, g, wide, s, norm_backward_rows(g.T, g.H, num_sms), st);
+  const int64_t grid = norm_backward_rows(g.T, g.H, num_sms);
+  const int smem = prepare(&g, s, wide, kBackwardThreads, grid);
+  return MOE_NORM_LAUNCH(norm_before_backward_kernel, g, wide, s, grid, smem, st);
 }
 
-cudaError_t launch_norm_after_backward(const NormAfterBackward& g, bool wide, int num_sms, cudaStream_t st) {
+cudaError_t launch_norm_after_backward(NormAfterBackward g, bool wide, int num_sms, cudaStream_t st) {
   const Shape s = shape_of(g.H);
-  return MOE_NORM_LAUNCH(norm_after_backward_kernel, g, wide, s, norm_backward_rows(g.T, g.H, num_sms), st);
+  const int64_t grid = norm_backward_rows(g.T, g.H, num_sms);
+  const int smem = prepare(&g, s, wide, kBackwardThreads, grid);
+  return MOE_NORM_LAUNCH(norm_after_backward_kernel, g, wide, s, grid, smem, st);
 }
 
 cudaError_t launch_column_sum(const ColumnSum& g, cudaStream_t st) {
