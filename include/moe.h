@@ -496,6 +496,44 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
                                      moe_tensor_t* dy, moe_tensor_t* dweight, moe_tensor_t* dgate,
                                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ---- a linear layer on microscaled 4-bit weights --------------------------
+ * Two forms of block scaling over e2m1 codes, by the scale_format argument:
+ *   MOE_SCALE_E8M0_32  one e8m0 scale (2^(code - 127)) per 32 elements: moe_quantize_mxfp4's
+ *                      (ROCm/aiter PR #3859, "Details": QuantType.per_1x32)
+ *   MOE_SCALE_E4M3_16  one e4m3 scale per 16 elements, times one float for the whole tensor
+ * In a MOE_E2M1X2 tensor of the second form `scale` points at the e4m3 codes.
+ *
+ * moe_quantize_nvfp4 writes the second form of the rows of src [R, K] (bf16 or f32, any
+ * strides, K % 32 == 0) with the given float G = global_scale[0] (usually amax / 2688, the
+ * whole tensor's largest value at code 6 and scale 448):
+ *   scale = e4m3(amax_16 / (6 G)),  code = e2m1(v / (scale G)),  value = code scale G
+ * both rounded to nearest of the exact quotient, ties to even, saturating; a block whose scale
+ * rounds to 0, and every block for G <= 0, becomes zeros.  dst's codes and scales have unit
+ * inner strides.  src holds finite numbers.
+ *
+ * moe_linear_fp4: out[t, n] = sum_k xq[t, k] wq[n, k], x quantised on the way in by the
+ * weight's form:
+ *   x              [T, K] bf16 or f32, any strides
+ *   weight         [N, K] MOE_E2M1X2, codes with unit inner stride, rows a multiple of 16 bytes
+ *                  apart, base 16-byte aligned; its scales [N, K/32 or K/16], any strides
+ *   x_global,      [1] or 0-d f32 on the device: the float scales of the e4m3 form (there x_global is
+ *   weight_global  required, weight_global NULL = 1); NULL with e8m0 scales
+ *   out            [T, N] bf16, any strides, rounded once from the fp32 sum
+ * K % 32 == 0.  Up to 4 tokens run as one launch, more as two (quantisation and placing of the
+ * scales; the product on the tensor cores).  Sums are fp32 in a fixed order.  `workspace`:
+ * moe_linear_fp4_workspace_bytes, 256-byte aligned (not read for up to 4 tokens unless
+ * T K > 72000 or so); it must not be shared by calls that run at the same time.  T = 0 is a
+ * no-op.  Asynchronous on `stream`, no allocation. */
+enum { MOE_SCALE_E8M0_32 = 0, MOE_SCALE_E4M3_16 = 1 };
+
+moe_status_t moe_quantize_nvfp4(const moe_tensor_t* src, const moe_tensor_t* global_scale,
+                                moe_tensor_t* dst, moe_stream_t stream);
+size_t moe_linear_fp4_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t scale_format);
+moe_status_t moe_linear_fp4(const moe_tensor_t* x, const moe_tensor_t* weight, int32_t scale_format,
+                            const moe_tensor_t* x_global, const moe_tensor_t* weight_global,
+                            moe_tensor_t* out, void* workspace, size_t workspace_bytes,
+                            moe_stream_t stream);
+
 /* Library version string. */
 const char* moe_version(void);
 

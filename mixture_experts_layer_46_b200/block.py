@@ -1,5 +1,6 @@
 """The operators around the expert forward (include/moe.h): the norms before and after a
-block with its gate and scaled residual, and their gradients.
+block with its gate and scaled residual, and their gradients; the linear layer on microscaled
+4-bit weights.
 
 Argument marshalling only, as in _abi.py.  Tensors that a call makes for its caller are
 allocated on the stream it runs on, on the inputs' device; every tensor of a call has to be on
@@ -13,7 +14,7 @@ import struct
 
 import torch
 
-from ._abi import MOE_BF16, MOE_F32, MOE_I32, MOE_I64, _check, load
+from ._abi import MOE_BF16, MOE_E2M1X2, MOE_F32, MOE_I32, MOE_I64, _check, load
 
 GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
 
@@ -36,6 +37,13 @@ def _desc(t: torch.Tensor | None):
         raise ValueError(f"a tensor of {n} dimensions")
     pad = (0, 0, 0, 0)[n:]
     return _TENSOR(t.data_ptr(), dt, n, *z, *pad, *s, *pad, 0, 0, 0, 0, 0)
+
+
+def _codes_desc(codes: torch.Tensor, scale: torch.Tensor):
+    """The bytes of a MOE_E2M1X2 matrix: two codes a byte, scales of one byte."""
+    z, s, q = codes.shape, codes.stride(), scale.stride()
+    return _TENSOR(codes.data_ptr(), MOE_E2M1X2, 2, z[0], 2 * z[1], 0, 0, s[0], s[1], 0, 0, scale.data_ptr(),
+                   q[0], q[1], 0, 0)
 
 
 def _raw_stream(index: int) -> int:
@@ -194,3 +202,61 @@ def norm_after_backward(dout, y, rstd, weight=None, gate=None, *, gate_act="none
             ws.numel() * ws.element_size() if want else 0, c.stream),
             "moe_norm_after_backward")
     return dy, dweight, dgate
+
+
+SCALE_E8M0_32, SCALE_E4M3_16 = 0, 1
+
+
+def _code_form(codes, scale):
+    """The scale format of a code matrix, from its scales' type; checks both tensors' sizes."""
+    if codes.dtype not in (torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8)):
+        raise ValueError(f"codes of type {codes.dtype}, not uint8 or float4_e2m1fn_x2")
+    if codes.dim() != 2 or scale.dim() != 2:
+        raise ValueError(f"codes of {codes.dim()} and scales of {scale.dim()} dimensions, not 2")
+    if scale.dtype == torch.float8_e4m3fn:
+        form, per = SCALE_E4M3_16, 16
+    elif scale.dtype in (torch.uint8, getattr(torch, "float8_e8m0fnu", torch.uint8)):
+        form, per = SCALE_E8M0_32, 32
+    else:
+        raise ValueError(f"scales of type {scale.dtype}: float8_e4m3fn per 16, or uint8 / float8_e8m0fnu per 32")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    if K % 32 != 0 or tuple(scale.shape) != (N, K // per):
+        raise ValueError(f"scales of shape {tuple(scale.shape)} for codes of {N} rows of {K} elements")
+    return form
+
+
+def quantize_nvfp4(src, global_scale=None, *, stream=None):
+    """(codes uint8 [R, K/2], scales float8_e4m3fn [R, K/16], global_scale f32 [1]) of src [R, K]
+    (bf16 or f32, K a multiple of 32): e2m1 codes, an e4m3 scale per 16, one float scale for the
+    tensor.  Without a given global_scale it is amax / 2688, which costs a pass over src."""
+    R, K = _rows(src, "src")
+    with _Call(stream, src, global_scale) as c:
+        if global_scale is None:
+            global_scale = ((src.abs().amax().float() if src.numel() else torch.zeros((), device=src.device))
+                            / 2688.0).reshape(1)
+        codes = c.empty(R, K // 2, dtype=torch.uint8)
+        scales = c.empty(R, K // 16, dtype=torch.float8_e4m3fn)
+        _check(load().moe_quantize_nvfp4(_desc(src), _desc(global_scale), _codes_desc(codes, scales), c.stream),
+               "moe_quantize_nvfp4")
+    return codes, scales, global_scale
+
+
+def linear_fp4_workspace_bytes(T: int, N: int, K: int, scale_format: int) -> int:
+    return int(load().moe_linear_fp4_workspace_bytes(T, N, K, scale_format))
+
+
+def linear_fp4(x, weight, weight_scale, *, x_global=None, w_global=None, out=None, workspace=None, stream=None):
+    """out [T, N] bf16 = x [T, K] (bf16 or f32, quantised on the way in) times the transposed 4-bit
+    weight [N, K]: codes uint8 [N, K/2] and, either e4m3 scales [N, K/16] (quantize_nvfp4; x_global
+    the float scale of x, w_global the weight's) or e8m0 scales [N, K/32] (quantize_mxfp4)."""
+    T, K = _rows(x, "x")
+    form = _code_form(weight, weight_scale)
+    with _Call(stream, x, weight, weight_scale, x_global, w_global, out, workspace) as c:
+        N = weight.shape[0]
+        if out is None:
+            out = c.empty(T, N, dtype=torch.bfloat16)
+        ws = c.workspace(workspace, linear_fp4_workspace_bytes(T, N, K, form))
+        _check(load().moe_linear_fp4(_desc(x), _codes_desc(weight, weight_scale), form, _desc(x_global),
+                                     _desc(w_global), _desc(out), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                     c.stream), "moe_linear_fp4")
+    return out

@@ -101,6 +101,21 @@ size_t norm_partial_bytes(int64_t T, int64_t H) {
   return round256((rows > 0 ? rows : 1) * static_cast<size_t>(H) * sizeof(float));
 }
 
+// A float32 scalar on the device ([1] or 0-d).
+moe_status_t scalar_of(const moe_tensor_t* t, const float** p) {
+  if (t->ndim > 1 || !t->data) return MOE_ERR_INVALID_ARG;
+  if (t->dtype != MOE_F32) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (t->ndim == 1 && t->sizes[0] != 1) return MOE_ERR_SHAPE_MISMATCH;
+  *p = static_cast<const float*>(t->data);
+  return MOE_OK;
+}
+
+constexpr int64_t kFp4MaxRows = int64_t(1) << 24, kFp4MaxK = int64_t(1) << 20;
+bool fp4_shape_ok(int64_t T, int64_t N, int64_t K, int32_t fmt) {
+  return T >= 0 && T <= kFp4MaxRows && N >= 1 && N <= kFp4MaxRows && K >= 32 && K <= kFp4MaxK && K % 32 == 0 &&
+         (fmt == MOE_SCALE_E8M0_32 || fmt == MOE_SCALE_E4M3_16);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -288,6 +303,114 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
     ++launches;
   }
   api_set_launches(launches);
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_nvfp4(const moe_tensor_t* src, const moe_tensor_t* global_scale, moe_tensor_t* dst,
+                                moe_stream_t stream) {
+  if (!src || !global_scale || !dst || src->ndim != 2 || dst->ndim != 2) return MOE_ERR_INVALID_ARG;
+  const int64_t R = src->sizes[0], K = src->sizes[1];
+  if (R < 0 || K < 0) return MOE_ERR_INVALID_ARG;
+  if (dst->dtype != MOE_E2M1X2) return MOE_ERR_UNSUPPORTED_DTYPE;
+  RowView x;
+  MOE_TRY(rows_of(src, R, K, false, &x));
+  if (dst->sizes[0] != R || dst->sizes[1] != K || K % 32 != 0) return MOE_ERR_SHAPE_MISMATCH;
+  const float* G = nullptr;
+  MOE_TRY(scalar_of(global_scale, &G));
+  if (R == 0 || K == 0) return MOE_OK;
+  if (!dst->data || !dst->scale) return MOE_ERR_INVALID_ARG;
+  if (dst->strides[1] != 1 || dst->scale_strides[1] != 1) return MOE_ERR_UNSUPPORTED_LAYOUT;
+  int sms = 0;
+  MOE_TRY(api_device(&sms, nullptr));
+  const cudaError_t rc = launch_quantize_nv(x, wide_ok(x), R, K, G, static_cast<uint8_t*>(dst->data), dst->strides[0],
+                                            static_cast<uint8_t*>(dst->scale), dst->scale_strides[0],
+                                            reinterpret_cast<cudaStream_t>(stream));
+  if (rc != cudaSuccess) return api_cuda_fail(rc, "quantize_nvfp4");
+  api_set_launches(1);
+  return MOE_OK;
+}
+
+size_t moe_linear_fp4_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t scale_format) {
+  if (!fp4_shape_ok(T, N, K, scale_format)) return 0;
+  const LinearFp4Plan p = linear_fp4_plan(T, N, K, scale_format == MOE_SCALE_E4M3_16);
+  return p.total > 256 ? p.total : 256;
+}
+
+moe_status_t moe_linear_fp4(const moe_tensor_t* x, const moe_tensor_t* weight, int32_t scale_format,
+                            const moe_tensor_t* x_global, const moe_tensor_t* weight_global, moe_tensor_t* out,
+                            void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (!x || !weight || !out || x->ndim != 2 || weight->ndim != 2 || out->ndim != 2) return MOE_ERR_INVALID_ARG;
+  const bool nv = scale_format == MOE_SCALE_E4M3_16;
+  if (!nv && scale_format != MOE_SCALE_E8M0_32) return MOE_ERR_INVALID_ARG;
+  if (nv ? !x_global : (x_global || weight_global)) return MOE_ERR_INVALID_ARG;
+  if (weight->dtype != MOE_E2M1X2 || out->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED_DTYPE;
+  LinearFp4 a = {};
+  a.T = x->sizes[0];
+  a.K = x->sizes[1];
+  a.N = weight->sizes[0];
+  a.nv = nv;
+  if (a.T < 0 || a.K < 0 || a.N < 0) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(rows_of(x, a.T, a.K, false, &a.x));
+  RowView o;
+  MOE_TRY(rows_of(out, a.T, a.N, true, &o));
+  if (weight->sizes[1] != a.K || !fp4_shape_ok(a.T, a.N, a.K, scale_format)) return MOE_ERR_SHAPE_MISMATCH;
+  if (x_global) MOE_TRY(scalar_of(x_global, &a.x_global));
+  if (weight_global) MOE_TRY(scalar_of(weight_global, &a.w_global));
+  if (!weight->data || !weight->scale) return MOE_ERR_INVALID_ARG;
+  if (weight->strides[1] != 1 || weight->strides[0] % 16 != 0 || weight->strides[0] < 0 ||
+      reinterpret_cast<uintptr_t>(weight->data) % 16 != 0)
+    return MOE_ERR_UNSUPPORTED_LAYOUT;
+  // (one row: its stride is never walked, but the copy engine wants one of at least a row)
+  a.w_ld = a.N == 1 && weight->strides[0] < a.K / 2 ? a.K / 2 : weight->strides[0];
+  if (a.w_ld < a.K / 2) return MOE_ERR_UNSUPPORTED_LAYOUT;
+  a.wide = wide_ok(a.x);
+  a.w = static_cast<const uint8_t*>(weight->data);
+  a.w_sf = static_cast<const uint8_t*>(weight->scale);
+  a.ws0 = weight->scale_strides[0];
+  a.ws1 = weight->scale_strides[1];
+  a.out = static_cast<__nv_bfloat16*>(out->data);
+  a.os0 = out->strides[0];
+  a.os1 = out->strides[1];
+  const bool rows = linear_fp4_by_rows(a.T, a.K);
+  const LinearFp4Plan p = linear_fp4_plan(a.T, a.N, a.K, nv);
+  if (!rows) {
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  if (a.T == 0) return MOE_OK;
+  int sms = 0;
+  MOE_TRY(api_device(&sms, &a.err));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t rc;
+  if (rows) {
+    rc = launch_linear_fp4_rows(a, sms, st);
+  } else {
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    CUtensorMap maps[4];
+    const uint64_t code_ld = static_cast<uint64_t>(p.num_k) * 128;
+    {
+      const uint64_t d[2] = {static_cast<uint64_t>(a.K / 2), static_cast<uint64_t>(a.T)}, sb[1] = {code_ld};
+      const uint32_t box[2] = {128, 128};
+      MOE_TRY(api_make_map(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w + p.codes_off, d, sb, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B));
+    }
+    {
+      const uint64_t d[2] = {static_cast<uint64_t>(a.K / 2), static_cast<uint64_t>(a.N)},
+                     sb[1] = {static_cast<uint64_t>(a.w_ld)};
+      const uint32_t box[2] = {128, static_cast<uint32_t>(p.ntile / 2)};
+      MOE_TRY(api_make_map(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.w, d, sb, box, CU_TENSOR_MAP_SWIZZLE_128B));
+    }
+    const uint32_t atoms = nv ? 4 : 2;
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t d[2] = {128, static_cast<uint64_t>(i == 0 ? p.x_atoms : p.w_atoms)}, sb[1] = {512};
+      const uint32_t box[2] = {128, i == 0 ? atoms : atoms * static_cast<uint32_t>(p.nh)};
+      MOE_TRY(api_make_map(&maps[2 + i], CU_TENSOR_MAP_DATA_TYPE_INT32, 2, w + (i == 0 ? p.x_off : p.w_off), d, sb,
+                           box, CU_TENSOR_MAP_SWIZZLE_NONE));
+    }
+    rc = launch_linear_fp4_pairs(a, p, maps, w, sms, st);
+  }
+  if (rc != cudaSuccess) return api_cuda_fail(rc, "linear_fp4");
+  api_set_launches(rows ? 1 : 2);
   return MOE_OK;
 }
 

@@ -105,4 +105,37 @@ cudaError_t launch_norm_before_backward(NormBeforeBackward g, bool wide, int num
 cudaError_t launch_norm_after_backward(NormAfterBackward g, bool wide, int num_sms, cudaStream_t st);
 cudaError_t launch_column_sum(const ColumnSum& g, cudaStream_t st);
 
+// ---- 4-bit linear layer (moe_linear_fp4.cu) -----------------------------------
+
+struct LinearFp4 {
+  RowView x;       // [T, K]
+  int wide;        // x allows 16-byte loads
+  int64_t T, N, K;
+  bool nv;         // e4m3 scales per 16 (else e8m0 per 32)
+  const float* x_global;  // nv: not null
+  const float* w_global;  // null: 1
+  const uint8_t* w;       // [N, K/2] codes, rows w_ld bytes apart
+  int64_t w_ld;
+  const uint8_t* w_sf;    // scales, byte strides
+  int64_t ws0, ws1;
+  __nv_bfloat16* out;
+  int64_t os0, os1;
+  DeviceErrors* err;
+};
+// Tiles and workspace of the tensor-core path (all zero where the few-rows kernel runs).
+struct LinearFp4Plan {
+  int64_t num_k, n_mt, n_nt;
+  int ntile, nh;
+  int64_t x_atoms, w_atoms;
+  size_t codes_off, x_off, w_off, total;
+};
+bool linear_fp4_by_rows(int64_t T, int64_t K);
+LinearFp4Plan linear_fp4_plan(int64_t T, int64_t N, int64_t K, bool nv);
+cudaError_t launch_linear_fp4_rows(const LinearFp4& a, int num_sms, cudaStream_t st);
+// maps: x codes, weight codes, x scale atoms, weight scale atoms
+cudaError_t launch_linear_fp4_pairs(const LinearFp4& a, const LinearFp4Plan& p, const CUtensorMap (&maps)[4],
+                                    uint8_t* ws, int num_sms, cudaStream_t st);
+cudaError_t launch_quantize_nv(const RowView& x, bool wide, int64_t rows, int64_t K, const float* global,
+                               uint8_t* codes, int64_t ld, uint8_t* sf, int64_t sf_ld, cudaStream_t st);
+
 }  // namespace moe

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_46_b200 as moe
-from mixture_experts_layer_46_b200.block import _desc
+from mixture_experts_layer_46_b200.block import _codes_desc, _desc
 
 BF, F32 = torch.bfloat16, torch.float32
 INVALID, SHAPE, DTYPE, LAYOUT, SMALL = 1, 2, 3, 4, 5
@@ -111,3 +111,87 @@ def test_wrappers_refuse_host_tensors_and_bad_names():
         moe.norm_after(x, x, gate_act="relu")
     with pytest.raises(ValueError, match="dimensions"):
         moe.norm_before(torch.zeros(4))
+
+
+# ---------------------------------------------------------------- the 4-bit linear layer
+
+U8 = torch.uint8
+
+
+def linear(x=None, w=None, sf=None, form=1, xg=0, wg=None, out=None, ws=None, n=None):
+    x = rows(8) if x is None else x
+    w = torch.zeros(48, 32, dtype=U8) if w is None else w
+    sf = torch.zeros(48, 4, dtype=U8) if sf is None else sf
+    xg = torch.zeros(1) if isinstance(xg, int) else xg
+    out = torch.zeros(8, 48, dtype=BF) if out is None else out
+    return moe.load().moe_linear_fp4(_desc(x), _codes_desc(w, sf) if w.dtype == U8 else _desc(w), form, _desc(xg),
+                                     _desc(wg), _desc(out), ws.data_ptr() if ws is not None else None,
+                                     (ws.numel() if n is None else n) if ws is not None else 0, None)
+
+
+@pytest.mark.parametrize("call,want", [
+    (lambda: linear(form=2), INVALID),
+    (lambda: linear(xg=None), INVALID),                       # e4m3 scales need x's float scale
+    (lambda: linear(form=0), INVALID),                        # e8m0 scales have none
+    (lambda: linear(form=0, xg=None, wg=torch.zeros(1)), INVALID),
+    (lambda: linear(xg=torch.zeros(2)), SHAPE),
+    (lambda: linear(xg=torch.zeros(1, dtype=BF)), DTYPE),
+    (lambda: linear(wg=torch.zeros(1, 1)), INVALID),
+    (lambda: linear(x=torch.zeros(64)), INVALID),
+    (lambda: linear(x=rows(8).half()), DTYPE),
+    (lambda: linear(w=rows(48, 64)), DTYPE),
+    (lambda: linear(out=torch.zeros(8, 48)), DTYPE),
+    (lambda: linear(out=torch.zeros(7, 48, dtype=BF)), SHAPE),
+    (lambda: linear(out=torch.zeros(8, 47, dtype=BF)), SHAPE),
+    (lambda: linear(x=rows(8, 96)), SHAPE),
+    (lambda: linear(x=rows(8, 48), w=torch.zeros(48, 24, dtype=U8)), SHAPE),  # K not a multiple of 32
+    (lambda: linear(out=torch.zeros(1, 48, dtype=BF).expand(8, 48)), LAYOUT),
+    (lambda: linear(w=torch.zeros(48, 40, dtype=U8)[:, :32]), LAYOUT),        # rows 40 bytes apart
+    (lambda: linear(w=torch.zeros(32, 48, dtype=U8).t()), LAYOUT),
+    (lambda: linear(w=torch.zeros(1, 32, dtype=U8).expand(48, 32)), LAYOUT),
+    (lambda: linear(), INVALID),                              # no workspace
+])
+def test_linear_refuses(call, want):
+    assert call() == want
+
+
+def test_linear_workspace():
+    n = moe.linear_fp4_workspace_bytes(8, 48, 64, moe.SCALE_E4M3_16)
+    raw = torch.zeros(n + 512, dtype=U8)
+    ws = raw[(-raw.data_ptr()) % 256:][:n]
+    assert linear(ws=ws, n=n - 1) == SMALL
+    assert linear(ws=raw[(-raw.data_ptr()) % 256 + 16:][:n]) == INVALID
+    assert moe.linear_fp4_workspace_bytes(8, 48, 48, 0) == 0
+    assert moe.linear_fp4_workspace_bytes(-1, 48, 64, 0) == 0
+    assert moe.linear_fp4_workspace_bytes(8, 48, 64, 7) == 0
+    # codes of x, its scales in whole blocks of 256 rows, the weight's scales
+    assert moe.linear_fp4_workspace_bytes(8192, 8192, 4096, 1) < 8192 * 2048 + 2 * 8960 * 256 + 4096
+
+
+def test_linear_wrapper_refuses():
+    x, w = rows(8), torch.zeros(48, 32, dtype=U8)
+    with pytest.raises(ValueError, match="shape"):
+        moe.linear_fp4(x, w, torch.zeros(48, 3, dtype=U8))
+    with pytest.raises(ValueError, match="shape"):
+        moe.linear_fp4(x, w, torch.zeros(48, 2, dtype=U8).view(torch.float8_e4m3fn))
+    with pytest.raises(ValueError, match="type"):
+        moe.linear_fp4(x, w, torch.zeros(48, 2))
+    with pytest.raises(ValueError, match="type"):
+        moe.linear_fp4(x, torch.zeros(48, 32), torch.zeros(48, 2, dtype=U8))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.linear_fp4(x, w, torch.zeros(48, 2, dtype=U8))
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.quantize_nvfp4(x)
+
+
+@pytest.mark.parametrize("src,G,dst,want", [
+    (rows(4, 48), torch.zeros(1), (4, 48), SHAPE),
+    (rows(4, 64), torch.zeros(2), (4, 64), SHAPE),
+    (rows(4, 64), torch.zeros(1), (5, 64), SHAPE),
+    (rows(4, 64).half(), torch.zeros(1), (4, 64), DTYPE),
+    (rows(4, 64), torch.zeros(1, dtype=BF), (4, 64), DTYPE),
+    (torch.zeros(64), torch.zeros(1), (4, 64), INVALID),
+])
+def test_quantize_refuses(src, G, dst, want):
+    codes, sf = torch.zeros(dst[0], dst[1] // 2, dtype=U8), torch.zeros(dst[0], dst[1] // 16, dtype=U8)
+    assert moe.load().moe_quantize_nvfp4(_desc(src), _desc(G), _codes_desc(codes, sf), None) == want
