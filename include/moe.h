@@ -496,6 +496,37 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
                                      moe_tensor_t* dy, moe_tensor_t* dweight, moe_tensor_t* dgate,
                                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ---- a whole mixture-of-experts layer for a few tokens -----------------------
+ * The layer around moe_forward (Liger-Kernel PR #1377, "Problems") at decoding sizes, from the
+ * residual stream to the residual stream, for T <= MOE_LAYER_MAX_TOKENS tokens:
+ *   xn     = x r pre_weight,  r_t = 1 / sqrt(mean x[t]^2 + eps)    (bf16 for the experts)
+ *   logits = xn router^T (64-bit sums, xn not rounded), the k largest chosen, a tie going to
+ *            the lower expert; topk_weights = softmax over all experts, or with renormalize = 1
+ *            over the chosen ones; shared_expert = 1 adds column k: expert E, weight 1
+ *   y      = moe_forward(xn, w13, w2, topk_ids, topk_weights)
+ *   out    = residual_scale x + a(gate) z,  z = y, or with post_norm = 1 y r' post_weight
+ *   x, out        [T, H] bf16, any strides; out may be x
+ *   pre_weight, post_weight  [H] bf16 or f32, any stride; NULL: ones (post_weight only with post_norm)
+ *   router        [E, H] bf16 or f32, any strides (bf16 rows 16 bytes aligned are read 16 bytes at
+ *                 a time); E <= 1024, H <= 16384, k + shared_expert <= 32
+ *   w13, w2       as for moe_forward_ws, E + shared_expert experts
+ *   gate, gate_act, residual_scale  as for moe_norm_after
+ *   topk_ids      [T, k + shared_expert] int32 or int64, topk_weights the same in f32; written
+ *   workspace     moe_layer_decode_workspace_bytes (E and k with the shared expert counted in),
+ *                 256-byte aligned; contents are scratch
+ * bf16 weights and at most 32 slots: two kernels (three with post_norm); else the forward's kernels
+ * between the first and the last.  Asynchronous on `stream`, no allocation.  T = 0 is a no-op. */
+enum { MOE_LAYER_MAX_TOKENS = 32 };
+
+size_t moe_layer_decode_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int32_t wdtype);
+moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_weight, float eps,
+                              const moe_tensor_t* router, int32_t k, int32_t renormalize,
+                              int32_t shared_expert, const moe_w13_t* w13, const moe_tensor_t* w2,
+                              int32_t post_norm, const moe_tensor_t* post_weight,
+                              const moe_tensor_t* gate, int32_t gate_act, float residual_scale,
+                              moe_tensor_t* topk_ids, moe_tensor_t* topk_weights, moe_tensor_t* out,
+                              void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* ---- a linear layer on microscaled 4-bit weights --------------------------
  * Two forms of block scaling over e2m1 codes, by the scale_format argument:
  *   MOE_SCALE_E8M0_32  one e8m0 scale (2^(code - 127)) per 32 elements: moe_quantize_mxfp4's

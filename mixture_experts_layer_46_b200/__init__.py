@@ -13,6 +13,6 @@ from ._abi import (MoeConfig, MoeError, MoeTensor, MoeW13, align, builtin_config
                    workspace_bytes, workspace_layout, debug_capture, MOE_CAPTURE_H_PREQUANT,
                    measure_mma_peak, backward, backward_input, backward_status, backward_workspace_bytes,
                    transpose_experts, host_workspace_bytes)
-from .block import (SCALE_E4M3_16, SCALE_E8M0_32, linear_fp4, linear_fp4_workspace_bytes, norm_after,  # noqa: F401
-                    norm_after_backward, norm_backward_workspace_bytes, norm_before, norm_before_backward,
-                    quantize_nvfp4)
+from .block import (SCALE_E4M3_16, SCALE_E8M0_32, layer_decode, layer_decode_workspace_bytes, linear_fp4,  # noqa: F401
+                    linear_fp4_workspace_bytes, norm_after, norm_after_backward,
+                    norm_backward_workspace_bytes, norm_before, norm_before_backward, quantize_nvfp4)

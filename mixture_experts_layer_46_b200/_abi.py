@@ -34,7 +34,7 @@ EXPORTS = ("moe_status_string", "moe_last_cuda_error", "moe_w13_from_packed",
            "moe_backward_input_ws", "moe_backward_ws", "moe_transpose_experts",
            "moe_host_workspace_bytes", "moe_forward_host_ws", "moe_norm_before", "moe_norm_after",
            "moe_norm_backward_workspace_bytes", "moe_norm_before_backward", "moe_norm_after_backward",
-           "moe_quantize_nvfp4", "moe_linear_fp4_workspace_bytes", "moe_linear_fp4")
+           "moe_layer_decode_workspace_bytes", "moe_layer_decode", "moe_quantize_nvfp4", "moe_linear_fp4_workspace_bytes", "moe_linear_fp4")
 STEP_NAMES = ("align", "permute", "gemm1_swiglu", "gemm2_weighted", "combine")
 
 
@@ -165,6 +165,10 @@ def load() -> ctypes.CDLL:
             lib.moe_norm_backward_workspace_bytes.argtypes = [i64, i64]
             lib.moe_norm_before_backward.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, vp, size, vp]
             lib.moe_norm_after_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, size, vp]
+            lib.moe_layer_decode_workspace_bytes.restype = size
+            lib.moe_layer_decode_workspace_bytes.argtypes = [i64] * 5 + [i32]
+            lib.moe_layer_decode.argtypes = [vp, vp, f32, vp, i32, i32, i32, P(MoeW13), vp, i32, vp, vp, i32, f32,
+                                             vp, vp, vp, vp, size, vp]
             lib.moe_quantize_nvfp4.argtypes = [vp, vp, vp, vp]
             lib.moe_linear_fp4_workspace_bytes.restype = size
             lib.moe_linear_fp4_workspace_bytes.argtypes = [i64, i64, i64, i32]

@@ -1,6 +1,6 @@
 """The operators around the expert forward (include/moe.h): the norms before and after a
-block with its gate and scaled residual, and their gradients; the linear layer on microscaled
-4-bit weights.
+block with its gate and scaled residual, and their gradients; a whole mixture-of-experts layer
+for a few tokens; the linear layer on microscaled 4-bit weights.
 
 Argument marshalling only, as in _abi.py.  Tensors that a call makes for its caller are
 allocated on the stream it runs on, on the inputs' device; every tensor of a call has to be on
@@ -10,11 +10,12 @@ that one device.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import struct
 
 import torch
 
-from ._abi import MOE_BF16, MOE_E2M1X2, MOE_F32, MOE_I32, MOE_I64, _check, load
+from ._abi import MOE_BF16, MOE_E2M1X2, MOE_F32, MOE_I32, MOE_I64, MoeW13, _check, load
 
 GATE_ACTS = {"none": 0, "sigmoid": 1, "tanh": 2}
 
@@ -44,6 +45,13 @@ def _codes_desc(codes: torch.Tensor, scale: torch.Tensor):
     z, s, q = codes.shape, codes.stride(), scale.stride()
     return _TENSOR(codes.data_ptr(), MOE_E2M1X2, 2, z[0], 2 * z[1], 0, 0, s[0], s[1], 0, 0, scale.data_ptr(),
                    q[0], q[1], 0, 0)
+
+
+def _experts_desc(codes: torch.Tensor, scale: torch.Tensor):
+    """The bytes of a MOE_E2M1X2 weight of all experts [E, rows, 2 * bytes]."""
+    z, s, q = codes.shape, codes.stride(), scale.stride()
+    return _TENSOR(codes.data_ptr(), MOE_E2M1X2, 3, z[0], z[1], 2 * z[2], 0, s[0], s[1], s[2], 0, scale.data_ptr(),
+                   q[0], q[1], q[2], 0)
 
 
 def _raw_stream(index: int) -> int:
@@ -202,6 +210,44 @@ def norm_after_backward(dout, y, rstd, weight=None, gate=None, *, gate_act="none
             ws.numel() * ws.element_size() if want else 0, c.stream),
             "moe_norm_after_backward")
     return dy, dweight, dgate
+
+
+def layer_decode_workspace_bytes(T: int, H: int, I: int, E: int, k: int, mxfp4: bool = False) -> int:
+    """E and k with the shared expert counted in."""
+    return int(load().moe_layer_decode_workspace_bytes(T, H, I, E, k, MOE_E2M1X2 if mxfp4 else MOE_BF16))
+
+
+def layer_decode(x, router, w13: MoeW13, w2, k: int, *, w2_scale=None, pre_weight=None, eps=1e-6, renormalize=True,
+                 shared_expert=False, post_norm=False, post_weight=None, gate=None, gate_act="none",
+                 residual_scale=1.0, out=None, topk_ids=None, topk_weights=None, workspace=None, stream=None):
+    """(out, topk_ids, topk_weights) of a whole mixture-of-experts layer on x [T, H] bf16, T <= 32:
+    norm, router [E, H], the k experts of largest softmax (and the shared expert E with weight 1),
+    their SwiGLU sum, and residual_scale * x + a(gate) * that sum (normed with post_norm).
+
+    w13 from w13_from_packed / w13_from_views, on x's device."""
+    T, H = _rows(x, "x")
+    E, _ = _rows(router, "router")
+    act = _act(gate_act)
+    n = 1 if shared_expert else 0
+    with _Call(stream, x, router, w2, w2_scale, pre_weight, post_weight, gate, out, topk_ids, topk_weights,
+               workspace) as c:
+        if out is None:
+            out = c.empty(T, H, dtype=torch.bfloat16)
+        if topk_ids is None:
+            topk_ids = c.empty(T, k + n, dtype=torch.int32)
+        if topk_weights is None:
+            topk_weights = c.empty(T, k + n, dtype=torch.float32)
+        if w2_scale is None:
+            d2, mx = _desc(w2), False
+        else:
+            d2, mx = _experts_desc(w2, w2_scale), True
+        ws = c.workspace(workspace, layer_decode_workspace_bytes(T, H, w13.gate.sizes[1], E + n, k + n, mx))
+        _check(load().moe_layer_decode(
+            _desc(x), _desc(pre_weight), eps, _desc(router), k, 1 if renormalize else 0, n, ctypes.byref(w13), d2,
+            1 if post_norm else 0, _desc(post_weight), _desc(gate), act, residual_scale, _desc(topk_ids),
+            _desc(topk_weights), _desc(out), ws.data_ptr(), ws.numel() * ws.element_size(), c.stream),
+            "moe_layer_decode")
+    return out, topk_ids, topk_weights
 
 
 SCALE_E8M0_32, SCALE_E4M3_16 = 0, 1

@@ -343,6 +343,7 @@ moe_status_t api_make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, co
   return make_map(map, dt, rank, base, dims, strides_bytes, box, swz);
 }
 void api_set_launches(int32_t n) { t_last_launches = n; }
+int32_t api_launches() { return t_last_launches; }
 
 // ---------------------------------------------------------------- layout
 
@@ -646,7 +647,8 @@ moe_status_t forward_mxfp4(const moe_tensor_t* x, const moe_w13_t* w13, const mo
 
 moe_status_t forward_impl(const moe_tensor_t* x, const moe_w13_t* w13, const moe_tensor_t* w2,
                           const moe_tensor_t* ids, const moe_tensor_t* wts, moe_tensor_t* out,
-                          const Problem& pr, void* ws, size_t ws_bytes, cudaStream_t st) {
+                          const Problem& pr, void* ws, size_t ws_bytes, cudaStream_t st,
+                          const Finish& finish = Finish()) {
   int launches = 0;
   t_last_launches = 0;
   if (pr.T == 0) return MOE_OK;
@@ -770,6 +772,7 @@ moe_status_t forward_impl(const moe_tensor_t* x, const moe_w13_t* w13, const moe
     dp.part_ws = reinterpret_cast<float*>(w + L.part);
     dp.max_split = cfg.split;
     dp.err = dev->errors;
+    dp.finish = finish;
     t_prof.n = 0;
     t_prof.have = false;
     prof_mark(st);
@@ -894,13 +897,32 @@ moe_status_t forward_impl(const moe_tensor_t* x, const moe_w13_t* w13, const moe
   prof_mark(st);
 
   rc = launch_combine(reinterpret_cast<const __nv_bfloat16*>(w + L.y), inv, pr.T, pr.H, pr.k,
-                      out->data, out->strides[0], out->strides[1], st, &launches);
+                      out->data, out->strides[0], out->strides[1], st, &launches, finish);
   if (rc != cudaSuccess) return cuda_fail(rc, "combine");
   prof_mark(st);
   t_prof.have = t_prof.on && t_prof.n == kProfSteps + 1;
   t_last_launches = launches;
   return MOE_OK;
 }
+
+}  // namespace
+
+moe_status_t api_forward_check(const moe_tensor_t* x, const moe_w13_t* w13, const moe_tensor_t* w2,
+                               const moe_tensor_t* ids, const moe_tensor_t* wts, const moe_tensor_t* out) {
+  Problem pr;
+  return validate(x, w13, w2, ids, wts, out, false, &pr);
+}
+moe_status_t api_forward(const moe_tensor_t* x, const moe_w13_t* w13, const moe_tensor_t* w2,
+                         const moe_tensor_t* ids, const moe_tensor_t* wts, moe_tensor_t* out, void* ws,
+                         size_t ws_bytes, cudaStream_t st, const Finish& finish) {
+  Problem pr;
+  const moe_status_t s = validate(x, w13, w2, ids, wts, out, false, &pr);
+  if (s != MOE_OK) return s;
+  if (pr.mxfp4 && finish.mode != kFinishNone) return MOE_ERR_UNSUPPORTED_DTYPE;
+  return forward_impl(x, w13, w2, ids, wts, out, pr, ws, ws_bytes, st, finish);
+}
+
+namespace {
 
 // ---------------------------------------------------------------- gradient (experts frozen)
 

@@ -414,4 +414,113 @@ moe_status_t moe_linear_fp4(const moe_tensor_t* x, const moe_tensor_t* weight, i
   return MOE_OK;
 }
 
+// [expert forward][normed rows bf16][the experts' rows: f32, or bf16 with MXFP4 weights]
+struct LayerWs {
+  size_t xn, y, total;
+};
+static bool layer_ws(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int32_t wdtype, LayerWs* w) {
+  if (T < 0 || T > MOE_LAYER_MAX_TOKENS || H > kRouteMaxH) return false;
+  const size_t fwd = moe_workspace_bytes(T > 0 ? T : 1, H, I, E, k, wdtype);
+  if (fwd == 0) return false;
+  w->xn = round256(fwd);
+  w->y = w->xn + round256(static_cast<size_t>(T) * H * 2);
+  w->total = w->y + round256(static_cast<size_t>(T) * H * 4);
+  return true;
+}
+
+size_t moe_layer_decode_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int32_t wdtype) {
+  LayerWs w;
+  return layer_ws(T, H, I, E, k, wdtype, &w) ? w.total : 0;
+}
+
+moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_weight, float eps,
+                              const moe_tensor_t* router, int32_t k, int32_t renormalize, int32_t shared_expert,
+                              const moe_w13_t* w13, const moe_tensor_t* w2, int32_t post_norm,
+                              const moe_tensor_t* post_weight, const moe_tensor_t* gate, int32_t gate_act,
+                              float residual_scale, moe_tensor_t* topk_ids, moe_tensor_t* topk_weights,
+                              moe_tensor_t* out, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (!x || !router || !w13 || !w2 || !topk_ids || !topk_weights || !out || x->ndim != 2 || router->ndim != 2 ||
+      topk_ids->ndim != 2 || topk_weights->ndim != 2 || !std::isfinite(eps) || eps < 0.0f ||
+      (renormalize != 0 && renormalize != 1) || (shared_expert != 0 && shared_expert != 1) ||
+      (post_norm != 0 && post_norm != 1) || (!post_norm && post_weight))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t T = x->sizes[0], H = x->sizes[1], E = router->sizes[0];
+  if (T < 0 || T > MOE_LAYER_MAX_TOKENS || H < 1 || H > kRouteMaxH || E < 1 || E > kRouteMaxE || k < 1 || k > E ||
+      k + shared_expert > 32)
+    return MOE_ERR_INVALID_ARG;
+  if (x->dtype != MOE_BF16 || out->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED_DTYPE;
+  Route r = {};
+  MOE_TRY(rows_of(x, T, H, false, &r.x));
+  MOE_TRY(rows_of(router, E, H, false, &r.router));
+  MOE_TRY(vector_of(pre_weight, H, false, &r.w));
+  RowView o, pw;
+  MOE_TRY(rows_of(out, T, H, true, &o));
+  MOE_TRY(vector_of(post_weight, H, false, &pw));
+  if (topk_ids->sizes[1] != k + shared_expert || w13->gate.sizes[0] != E + shared_expert) return MOE_ERR_SHAPE_MISMATCH;
+  for (const moe_tensor_t* t : {topk_ids, topk_weights})
+    if ((T > 1 && t->strides[0] == 0) || (k + shared_expert > 1 && t->strides[1] == 0)) return MOE_ERR_UNSUPPORTED_LAYOUT;
+  MOE_TRY(api_forward_check(x, w13, w2, topk_ids, topk_weights, out));
+  RowView gv;
+  int gate_mode = 0;
+  MOE_TRY(gate_of(gate, T, H, gate_act, &gv, &gate_mode));
+  const int32_t wd = w13->gate.dtype;
+  const int64_t I = w13->gate.sizes[1];
+  LayerWs L;
+  if (!layer_ws(T, H, I, E + shared_expert, k + shared_expert, wd, &L)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (T == 0) return MOE_OK;
+  int sms = 0;
+  MOE_TRY(api_device(&sms, nullptr));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  r.wide = r.router.dtype == MOE_BF16 && r.w.dtype == MOE_BF16 && H % 8 == 0 && wide_ok(r.router);
+  r.T = T;
+  r.H = static_cast<int>(H);
+  r.E = static_cast<int>(E);
+  r.k = k;
+  r.renorm = renormalize;
+  r.shared = shared_expert;
+  r.eps = eps;
+  r.xn = reinterpret_cast<__nv_bfloat16*>(ws + L.xn);
+  r.ids = View2{topk_ids->data, topk_ids->strides[0], topk_ids->strides[1], topk_ids->dtype};
+  r.wts = View2{topk_weights->data, topk_weights->strides[0], topk_weights->strides[1], topk_weights->dtype};
+  const cudaError_t rc = launch_route(r, st);
+  if (rc != cudaSuccess) return api_cuda_fail(rc, "layer_decode route");
+  int launches = 1;
+  moe_tensor_t xn = {};
+  xn.data = ws + L.xn;
+  xn.dtype = MOE_BF16;
+  xn.ndim = 2;
+  xn.sizes[0] = T;
+  xn.sizes[1] = H;
+  xn.strides[0] = H;
+  xn.strides[1] = 1;
+  moe_tensor_t y = xn;
+  y.data = ws + L.y;
+  // the experts' sum: finished where the slots are combined, or kept for the norm after it
+  Finish f;
+  const bool after = post_norm || wd != MOE_BF16;
+  if (!after) {
+    f.mode = kFinishGate;
+    f.residual = View2{x->data, x->strides[0], x->strides[1], x->dtype};
+    f.alpha = residual_scale;
+    f.gate = View2{gv.data, gv.s0, gv.s1, gv.dtype};
+    f.act = gate_act;
+  } else if (wd == MOE_BF16) {
+    f.mode = kFinishRows;
+    f.y32 = reinterpret_cast<float*>(ws + L.y);
+  }
+  MOE_TRY(api_forward(&xn, w13, w2, topk_ids, topk_weights, after ? &y : out, workspace, L.xn, st, f));
+  launches += api_launches();
+  if (after) {
+    if (f.mode == kFinishRows) y.dtype = MOE_F32;
+    MOE_TRY(moe_norm_after(&y, x, post_weight, gate, gate_act, post_norm, residual_scale, eps, out, nullptr, nullptr,
+                           nullptr, nullptr, stream));
+    ++launches;
+  }
+  api_set_launches(launches);
+  return MOE_OK;
+}
+
 }  // extern "C"

@@ -8,6 +8,7 @@
 
 #include "../../include/moe.h"
 #include "moe_common.cuh"
+#include "moe_internal.h"
 
 namespace moe {
 
@@ -22,6 +23,13 @@ moe_status_t api_make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, co
                           const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
                           CUtensorMapSwizzle swz);
 void api_set_launches(int32_t n);
+int32_t api_launches();
+// The expert forward with a finish (bf16 weights; MXFP4 weights: none), and its checks alone.
+moe_status_t api_forward_check(const moe_tensor_t* x, const moe_w13_t* w13, const moe_tensor_t* w2,
+                               const moe_tensor_t* ids, const moe_tensor_t* wts, const moe_tensor_t* out);
+moe_status_t api_forward(const moe_tensor_t* x, const moe_w13_t* w13, const moe_tensor_t* w2,
+                         const moe_tensor_t* ids, const moe_tensor_t* wts, moe_tensor_t* out, void* ws,
+                         size_t ws_bytes, cudaStream_t st, const Finish& finish);
 
 // ---- norms (moe_norm.cu) -----------------------------------------------------
 
@@ -104,6 +112,20 @@ cudaError_t launch_norm_after(NormAfter g, bool wide, int num_sms, cudaStream_t 
 cudaError_t launch_norm_before_backward(NormBeforeBackward g, bool wide, int num_sms, cudaStream_t st);
 cudaError_t launch_norm_after_backward(NormAfterBackward g, bool wide, int num_sms, cudaStream_t st);
 cudaError_t launch_column_sum(const ColumnSum& g, cudaStream_t st);
+
+// ---- a layer's way in: norm, router, choice (moe_route.cu) --------------------
+
+constexpr int64_t kRouteMaxH = 16384, kRouteMaxE = 1024;
+struct Route {
+  RowView x, w, router;  // w: no data = ones; router [E, H]
+  int wide;              // router: bf16, 16-byte rows
+  int64_t T;
+  int H, E, k, renorm, shared;
+  float eps;
+  __nv_bfloat16* xn;     // [T, H]
+  View2 ids, wts;
+};
+cudaError_t launch_route(const Route& g, cudaStream_t st);
 
 // ---- 4-bit linear layer (moe_linear_fp4.cu) -----------------------------------
 

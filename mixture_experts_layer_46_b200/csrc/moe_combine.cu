@@ -5,6 +5,7 @@
 // epilogue.  No atomics, so the result is identical run to run and does not
 // depend on how the slots were grouped.  out is written through its strides.
 #include "../../include/moe.h"
+#include "moe_gate.cuh"
 #include "moe_internal.h"
 
 namespace moe {
@@ -27,7 +28,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __nv_bfloat16* __res
                                                       const int32_t* __restrict__ inv, int64_t T,
                                                       int64_t H, int64_t k,
                                                       __nv_bfloat16* __restrict__ out, int64_t os0,
-                                                      int64_t os1, int vec_out) {
+                                                      int64_t os1, int vec_out, const Finish finish) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t H8 = H / 8;
@@ -53,6 +54,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __nv_bfloat16* __res
         const int32_t r = __ldg(rows + j);
         if (r >= 0) acc_bf16x8(a, __ldg(reinterpret_cast<const uint4*>(y + static_cast<int64_t>(r) * H) + c));
       }
+      if (finish8(finish, t, H, c * 8, a)) continue;
       if (vec_out) {
         uint4 o;
         o.x = pack_bf16x2(a[0], a[1]);
@@ -72,14 +74,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const __nv_bfloat16* __res
 
 cudaError_t launch_combine(const __nv_bfloat16* y, const int32_t* inv, int64_t T, int64_t H,
                            int64_t k, void* out, int64_t os0, int64_t os1, cudaStream_t st,
-                           int* launches) {
+                           int* launches, const Finish& finish) {
   const int vec_out = (os1 == 1) && ((os0 * 2) % 16 == 0) &&
                       (reinterpret_cast<uintptr_t>(out) % 16 == 0);
   int64_t blocks = T < 65535 ? T : 65535;
   if (blocks < 1) blocks = 1;
   if (launches) *launches += 1;
   return launch_pdl(combine_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, y, inv,
-                    T, H, k, static_cast<__nv_bfloat16*>(out), os0, os1, vec_out);
+                    T, H, k, static_cast<__nv_bfloat16*>(out), os0, os1, vec_out, finish);
 }
 
 }  // namespace moe

@@ -34,6 +34,7 @@
 
 #include "../../include/moe.h"
 #include "moe_decode_units.cuh"
+#include "moe_gate.cuh"
 #include "moe_internal.h"
 
 namespace moe {
@@ -78,6 +79,7 @@ struct DecArgs {
   float* part_ws;        // GEMM1 split-K partials (layout of decode_part_bytes)
   int32_t max_split;     // at most this many GEMM1 K parts
   DeviceErrors* err;
+  Finish finish;
 };
 
 __device__ __forceinline__ int64_t read_id(const View2& v, int64_t s, int64_t k) {
@@ -554,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc[2 * i + 1] += __uint_as_float(w4[i] & 0xffff0000u);
               }
             }
+            if (finish8(g.finish, t, g.H, c, acc)) continue;
             if (g.vec_out) {
               uint4 o;
               o.x = pack_bf16x2(acc[0], acc[1]);
@@ -645,6 +648,7 @@ cudaError_t launch_decode_fused(const CUtensorMap& gate, const CUtensorMap& up, 
   g.part_ws = p.part_ws;
   g.max_split = p.max_split;
   g.err = p.err;
+  g.finish = p.finish;
   if (launches) *launches += 1;
   return launch_pdl(moe_decode_fused_kernel, dim3(static_cast<unsigned>(num_sms)), dim3(kThreads), kSmem,
                     st, gate, up, w2, x1, h1, g);

@@ -18,6 +18,18 @@ struct View2 {
   int32_t dtype;   // MOE_* code
 };
 
+// What the combine of the slots' rows does with a sum: out as it is, the sum unrounded to y32
+// [T, H] instead, or out = alpha * residual + a(gate) * sum (moe_gate.cuh).
+enum { kFinishNone = 0, kFinishRows = 1, kFinishGate = 2 };
+struct Finish {
+  int mode = kFinishNone;
+  float* y32 = nullptr;
+  View2 residual = {};  // bf16
+  float alpha = 0.0f;
+  View2 gate = {};      // stride 0 along a broadcast axis; no data: 1
+  int act = 0;
+};
+
 // Byte layout of the forward's workspace.  Every region starts on a 256-byte
 // boundary.  Sizes depend only on (T, H, I, E, k, weight dtype).
 struct WsLayout {
@@ -129,7 +141,7 @@ cudaError_t launch_transpose_experts(const void* src, int64_t s0, int64_t s1, vo
 // combine: out[t, :] = sum_j y[inv[t*k + j], :] over valid slots (fixed j order)
 cudaError_t launch_combine(const __nv_bfloat16* y, const int32_t* inv, int64_t T, int64_t H,
                            int64_t k, void* out, int64_t os0, int64_t os1, cudaStream_t st,
-                           int* launches);
+                           int* launches, const Finish& finish = Finish());
 
 // Weight-stationary ("swap AB") bf16 GEMMs over the token-tile list of align.
 struct WsGemm {
@@ -235,6 +247,7 @@ struct DecodeArgs {
   float* part_ws;     // GEMM1 split-K partials (decode_part_bytes(I))
   int32_t max_split;  // at most this many GEMM1 K parts (1: not split)
   DeviceErrors* err;
+  Finish finish;
 };
 // maps: gate/up/w2 3-D weight maps ([64 x 128] boxes), x1 = x [T, H] and h1 = h_ws [32, I]
 // with one-row [64 x 1] boxes (read by four-row gathers); grid = num_sms

@@ -24,6 +24,7 @@
 
 #include "../../include/moe.h"
 #include "moe_block.h"
+#include "moe_gate.cuh"
 #include "moe_internal.h"
 
 namespace moe {
@@ -232,12 +233,7 @@ __device__ __forceinline__ float scalar_at(const RowView& t, int64_t off) {
                             : bf16_lo(static_cast<const uint16_t*>(t.data)[off]);
 }
 
-// the gate's activation and its derivative, from the gate's value
-__device__ __forceinline__ float gate_value(float g, int act) {
-  if (act == MOE_GATE_SIGMOID) return 1.0f / (1.0f + expf(-g));
-  if (act == MOE_GATE_TANH) return tanhf(g);
-  return g;
-}
+// the derivative of the gate's activation, from the gate's value
 // (the slopes from e = exp(-|.|), which keeps their relative accuracy where the function is flat:
 // sigmoid' = e / (1 + e)^2 with e = exp(-|g|), tanh' = 4 e / (1 + e)^2 with e = exp(-2 |g|))
 __device__ __forceinline__ float gate_slope(float g, int act) {

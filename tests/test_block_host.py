@@ -195,3 +195,63 @@ def test_linear_wrapper_refuses():
 def test_quantize_refuses(src, G, dst, want):
     codes, sf = torch.zeros(dst[0], dst[1] // 2, dtype=U8), torch.zeros(dst[0], dst[1] // 16, dtype=U8)
     assert moe.load().moe_quantize_nvfp4(_desc(src), _desc(G), _codes_desc(codes, sf), None) == want
+
+
+# ---------------------------------------------------------------- a whole layer for a few tokens
+
+def layer(T=2, H=64, I=32, E=4, k=2, x=None, pre=None, eps=1e-6, router=None, renorm=1, shared=0, post=0, pw=None,
+          gate=None, act=0, ids=None, wts=None, out=None, w13=None, w2=None, ws=None, n=None):
+    import ctypes
+
+    x = rows(T, H) if x is None else x
+    router = rows(E, H) if router is None else router
+    w13 = torch.zeros(E + shared, 2 * I, H, dtype=BF) if w13 is None else w13
+    w2 = torch.zeros(E + shared, H, I, dtype=BF) if w2 is None else w2
+    ids = torch.zeros(T, k + shared, dtype=torch.int32) if ids is None else ids
+    wts = torch.zeros(T, k + shared) if wts is None else wts
+    out = rows(T, H) if out is None else out
+    return moe.load().moe_layer_decode(
+        _desc(x), _desc(pre), eps, _desc(router), k, renorm, shared, ctypes.byref(moe.w13_from_packed(w13)), _desc(w2),
+        post, _desc(pw), _desc(gate), act, 1.0, _desc(ids), _desc(wts), _desc(out),
+        ws.data_ptr() if ws is not None else None, (ws.numel() if n is None else n) if ws is not None else 0, None)
+
+
+@pytest.mark.parametrize("call,want", [
+    (lambda: layer(T=33), INVALID),
+    (lambda: layer(k=5), INVALID),
+    (lambda: layer(k=0, ids=torch.zeros(2, 1, dtype=torch.int32), wts=torch.zeros(2, 1)), INVALID),
+    (lambda: layer(E=40, k=32, shared=1), INVALID),
+    (lambda: layer(E=1025), INVALID),
+    (lambda: layer(eps=float("nan")), INVALID),
+    (lambda: layer(renorm=2), INVALID),
+    (lambda: layer(act=5), INVALID),
+    (lambda: layer(pw=torch.zeros(64)), INVALID),                       # a post weight without the post norm
+    (lambda: layer(x=torch.zeros(2, 64)), DTYPE),
+    (lambda: layer(router=torch.zeros(4, 64, dtype=torch.float16)), DTYPE),
+    (lambda: layer(ids=torch.zeros(2, 2)), DTYPE),
+    (lambda: layer(wts=torch.zeros(2, 2, dtype=BF)), DTYPE),
+    (lambda: layer(router=rows(4, 32)), SHAPE),
+    (lambda: layer(pre=torch.zeros(63)), SHAPE),
+    (lambda: layer(ids=torch.zeros(2, 3, dtype=torch.int32)), SHAPE),
+    (lambda: layer(w13=torch.zeros(5, 64, 64, dtype=BF)), SHAPE),
+    (lambda: layer(w2=torch.zeros(4, 64, 64, dtype=BF)), SHAPE),
+    (lambda: layer(gate=torch.zeros(3, 64)), SHAPE),
+    (lambda: layer(out=rows(2, 32)), SHAPE),
+    (lambda: layer(ids=torch.zeros(1, 2, dtype=torch.int32).expand(2, 2)), LAYOUT),
+    (lambda: layer(out=torch.zeros(1, 64, dtype=BF).expand(2, 64)), LAYOUT),
+    (lambda: layer(), INVALID),                                         # no workspace
+])
+def test_layer_refuses(call, want):
+    assert call() == want
+
+
+def test_layer_workspace():
+    n = moe.layer_decode_workspace_bytes(2, 64, 32, 4, 2)
+    raw = torch.zeros(n + 512, dtype=U8)
+    ws = raw[(-raw.data_ptr()) % 256:][:n]
+    assert layer(ws=ws, n=n - 1) == SMALL
+    assert layer(ws=raw[(-raw.data_ptr()) % 256 + 16:][:n]) == INVALID
+    assert moe.layer_decode_workspace_bytes(33, 64, 32, 4, 2) == 0
+    assert moe.layer_decode_workspace_bytes(2, 16416, 32, 4, 2) == 0
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.layer_decode(rows(2), rows(4), moe.w13_from_packed(torch.zeros(4, 64, 64, dtype=BF)), torch.zeros(4, 64, 32, dtype=BF), 2)
