@@ -9,6 +9,7 @@ or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import struct
 import os
 import threading
 
@@ -191,32 +192,29 @@ _TORCH_DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.int32: MOE_
              torch.int64: MOE_I64}
 
 
+# moe_tensor_t: data, dtype, ndim, sizes[4], strides[4], scale, scale_strides[4]
+_TENSOR = struct.Struct("=Qii4q4qQ4q").pack
+_PACKED_DT = tuple(getattr(torch, n) for n in ("uint8", "float4_e2m1fn_x2") if hasattr(torch, n))
+
+
 def desc(t: torch.Tensor, scale: torch.Tensor | None = None) -> MoeTensor:
     """moe_tensor_t for a torch tensor.  uint8 (or float4_e2m1fn_x2) tensors are
     packed e2m1 pairs: the logical innermost size is twice the byte count and
     `scale` (uint8 e8m0 codes, one per 32 logical elements) is required."""
-    d = MoeTensor()
-    d.data = t.data_ptr() if t.numel() > 0 else None
-    d.ndim = t.dim()
-    if hasattr(torch, "float4_e2m1fn_x2") and t.dtype == torch.float4_e2m1fn_x2:
-        t = t.view(torch.uint8)
-    if t.dtype == torch.uint8:
-        d.dtype = MOE_E2M1X2
+    if t.dtype in _PACKED_DT:
         if scale is None:
             raise ValueError("an e2m1 tensor needs its e8m0 scale tensor")
-        if scale.dtype != torch.uint8:
-            scale = scale.view(torch.uint8)
-        d.scale = scale.data_ptr()
-        for i in range(scale.dim()):
-            d.scale_strides[i] = scale.stride(i)
+        dt, sp, sq = MOE_E2M1X2, scale.data_ptr(), scale.stride()
     else:
-        d.dtype = _TORCH_DT.get(t.dtype, 99)  # unknown dtypes are rejected by the library
-    for i in range(t.dim()):
-        d.sizes[i] = t.shape[i]
-        d.strides[i] = t.stride(i)
-    if d.dtype == MOE_E2M1X2:
-        d.sizes[t.dim() - 1] = 2 * t.shape[-1]
-    return d
+        dt, sp, sq = _TORCH_DT.get(t.dtype, 99), 0, ()  # unknown dtypes are rejected by the library
+    n, z, s = t.dim(), t.shape, t.stride()
+    if n > 4 or len(sq) > 4:
+        raise ValueError(f"a tensor of {n} dimensions")
+    if dt == MOE_E2M1X2:
+        z = (*z[:-1], 2 * z[-1])
+    pad = (0, 0, 0, 0)
+    return MoeTensor.from_buffer_copy(_TENSOR(t.data_ptr() if t.numel() > 0 else 0, dt, n, *z, *pad[n:], *s, *pad[n:],
+                                              sp, *sq, *pad[len(sq):]))
 
 
 def _stream_ptr(stream) -> int | None:

@@ -5,7 +5,7 @@
 Every .cu under csrc/ is compiled for sm_100a (-gencode arch=compute_100a,
 code=sm_100a, -lineinfo) into one object each, in parallel, then linked into
 mixture_experts_layer_46_b200/libmoe_b200.so with the CUDA runtime linked
-statically.  Objects go to _build/ (git-ignored).
+statically; csrc/moe_torch.cpp becomes the Python module _moe_torch.so beside it.  Objects go to _build/ (git-ignored).
 
 The tuned kernel-configuration table (configs/b200_tuned.csv, written by
 tune.py) is turned into a C array, _build/moe_config_table.inc, that the
@@ -27,6 +27,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
+BINDING = os.path.join(PKG, "_moe_torch.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 CONFIG_CSV = os.path.join(PKG, "configs", "b200_tuned.csv")
@@ -139,7 +140,33 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The Python module over the operators around the forward (csrc/moe_torch.cpp)."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "moe_torch.cpp")
+    if not (force or _stale(BINDING, [src, os.path.join(INCLUDE, "moe.h")])):
+        return BINDING
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
+    lib = os.path.join(base, "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in inc:
+        cmd += ["-isystem" if d != INCLUDE else "-I", d]
+    cmd += [src, "-o", BINDING, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-L" + PKG,
+            "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return BINDING
 
 
 if __name__ == "__main__":
