@@ -4,8 +4,8 @@
 //   s = e4m3(amax / (6 G)),  code = e2m1(v / (s G)),   value = code * s * G
 // Both roundings go to the nearest number, ties to the even one, of the exact quotient.  In
 // fp32 a quotient is off by up to 2^-22, so each is rounded twice, moved down and up by 2^-20:
-// equal results are the exact one's too, and where they differ (one in some thousand times) the
-// quotient is compared with the border between the two neighbours exactly.
+// equal results are the exact one's too, and where they differ the quotient is compared with the
+// border between the two neighbours exactly.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -38,16 +38,38 @@ __device__ __forceinline__ uint32_t e2m1x2_halves(uint32_t byte) {
   return h;
 }
 
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  return static_cast<uint64_t>(__float_as_uint(a)) | (static_cast<uint64_t>(__float_as_uint(b)) << 32);
+}
+// the e2m1 codes of eight floats times f, the first in the low nibble (+ 0: a zero has no sign)
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v, float f) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b64 t, z;\n\t.reg .f32 x, y;\n\t"
+      "mov.b64 z, 0;\n\t"
+      "fma.rn.f32x2 t, %1, %5, z;\n\tmov.b64 {x, y}, t;\n\tcvt.rn.satfinite.e2m1x2.f32 b0, y, x;\n\t"
+      "fma.rn.f32x2 t, %2, %5, z;\n\tmov.b64 {x, y}, t;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, y, x;\n\t"
+      "fma.rn.f32x2 t, %3, %5, z;\n\tmov.b64 {x, y}, t;\n\tcvt.rn.satfinite.e2m1x2.f32 b2, y, x;\n\t"
+      "fma.rn.f32x2 t, %4, %5, z;\n\tmov.b64 {x, y}, t;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, y, x;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "l"(pair_of(v[0], v[1])), "l"(pair_of(v[2], v[3])), "l"(pair_of(v[4], v[5])), "l"(pair_of(v[6], v[7])),
+        "l"(pair_of(f, f)));
+  return r;
+}
+
 constexpr float kDown = 1.0f - 1.0f / (1 << 20), kUp = 1.0f + 1.0f / (1 << 20);
 
-// e4m3 code of amax / (6 G); G a positive finite float, amax >= 0
-__device__ __forceinline__ uint32_t nv_scale(float amax, float G) {
-  const float r = amax / (6.0f * G);
-  const uint32_t two = cvt_e4m3x2(r * kDown, r * kUp);
-  const uint32_t lo = two & 0xffu, hi = two >> 8;
-  const float g6 = 6.0f * G;
-  if (lo == hi && g6 < 1e30f && g6 > 1e-30f) return lo;
-  // exactly: the neighbours around the quotient in 64 bits
+// e4m3 code of amax / (6 G); G a positive finite float, inv6 = 1 / (6 G), amax >= 0.
+// Six times the border between neighbours has at most 7 bits: exact as below.
+__device__ __forceinline__ uint32_t nv_scale(float amax, float G, float inv6) {
+  const float r = amax * inv6;
+  const uint32_t two = cvt_e4m3x2(r * kDown, r * kUp), lo = two & 0xffu, hi = two >> 8;
+  const float2 v = e4m3x2_floats(two);
+  const float d = fmaf(-3.0f * (v.x + v.y), G, amax);
+  return d > 0.0f || (d == 0.0f && (lo & 1u)) ? hi : lo;
+}
+// The same where 6 G or its inverse leaves the range that keeps fp32 products exact.
+__device__ __noinline__ uint32_t nv_scale_far(float amax, float G) {
   const double t = static_cast<double>(amax) / (6.0 * static_cast<double>(G));
   if (!(t < 448.0)) return 0x7eu;
   uint32_t c = 0;
@@ -58,49 +80,64 @@ __device__ __forceinline__ uint32_t nv_scale(float amax, float G) {
   const double mid = 0.5 * (static_cast<double>(v.x) + static_cast<double>(v.y));
   return t > mid || (t == mid && (c & 1u)) ? c + 1 : c;
 }
-
-// e2m1 magnitude code of |v| / (s G), exactly: |v| is compared with border * s * G by a fused
-// multiply-add, whose sign is that of the exact difference (border * s has at most 7 bits).
-__device__ __forceinline__ uint32_t e2m1_exact(float v, float s, float G) {
-  const float border[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.0f};
+__device__ __noinline__ uint32_t e2m1_far(float v, float s, float G) {
+  const double t = fabs(static_cast<double>(v)) / (static_cast<double>(s) * static_cast<double>(G));
+  const double border[7] = {0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0};
   uint32_t c = 0;
-#pragma unroll
-  for (int i = 0; i < 7; ++i) {
-    const float d = fmaf(-(border[i] * s), G, fabsf(v));
-    if (d > 0.0f || (d == 0.0f && (i & 1))) c = i + 1;  // a tie goes to the even code
-  }
+  for (int i = 0; i < 7; ++i)
+    if (t > border[i] || (t == border[i] && (i & 1))) c = i + 1;  // a tie goes to the even code
   return c | (v < 0.0f ? 8u : 0u);
 }
 
-// Quantises 16 floats: two words of codes (even element in the low nibble), returns the scale.
-__device__ __forceinline__ uint32_t nv_quant16(const float* v, float G, uint32_t (&w)[2]) {
-  float amax = 0.0f;
+// Sixteen codes of v / (s G).  Where the two roundings differ, |v| is compared with border * s * G
+// by a fused multiply-add, whose sign is that of the exact difference (border * s has 7 bits).
+// Ties are not rare: with G = amax / 2688 and bf16 values they meet one block in a hundred.
+__device__ __forceinline__ void nv_codes16(const float* v, float s, float G, float down, float up, uint32_t (&w)[2]) {
+  w[0] = cvt_e2m1x8(v, down);
+  w[1] = cvt_e2m1x8(v + 8, down);
+  const uint32_t d0 = w[0] ^ cvt_e2m1x8(v, up), d1 = w[1] ^ cvt_e2m1x8(v + 8, up);
+  if ((d0 | d1) == 0u) return;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  w[0] = w[1] = 0u;
-  if (!(G > 0.0f) || !(amax > 0.0f)) return 0u;
-  const uint32_t sc = nv_scale(amax, G);
-  if (sc == 0u) return 0u;
-  const float s = e4m3x2_floats(sc).x, unit = s * G;
-  const float inv = 1.0f / unit, a = inv * kDown, b = inv * kUp;
-  uint32_t up[2] = {0u, 0u};
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t diff = q ? d1 : d0;
+    if (diff == 0u) continue;
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float e = v[8 * q + 2 * i], o = v[8 * q + 2 * i + 1];
-      w[q] |= cvt_e2m1x2(e * a, o * a) << (8 * i);
-      up[q] |= cvt_e2m1x2(e * b, o * b) << (8 * i);
-    }
-  if (w[0] != up[0] || w[1] != up[1] || !(unit > 1e-30f && unit < 1e30f)) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      w[q] = 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[q] |= e2m1_exact(v[8 * q + i], s, G) << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+      if (((diff >> (4 * i)) & 15u) == 0u) continue;
+      const uint32_t l = (w[q] >> (4 * i)) & 7u, h = ((w[q] ^ diff) >> (4 * i)) & 7u;
+      const uint32_t two = e2m1x2_halves(l | (h << 4));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+      const float d = fmaf(-(0.5f * (f.x + f.y) * s), G, fabsf(v[8 * q + i]));
+      if (d > 0.0f || (d == 0.0f && (l & 1u))) w[q] ^= diff & (15u << (4 * i));
     }
   }
+}
+
+// Quantises 16 floats whose largest magnitude is amax: two words of codes (even element in the
+// low nibble), returns the scale.  inv6 = 1 / (6 G).
+__device__ __forceinline__ uint32_t nv_quant16(const float* v, float amax, float G, float inv6, uint32_t (&w)[2]) {
+  w[0] = w[1] = 0u;
+  if (!(G > 0.0f) || !(amax > 0.0f)) return 0u;
+  const bool far = !(G > 1e-24f && G < 1e24f);
+  const uint32_t sc = far ? nv_scale_far(amax, G) : nv_scale(amax, G, inv6);
+  if (sc == 0u) return 0u;
+  const float s = e4m3x2_floats(sc).x;
+  if (!far) {
+    const float inv = __frcp_rn(s * G), down = inv * kDown, up = inv * kUp;
+    nv_codes16(v, s, G, down, up, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i >> 3] |= e2m1_far(v[i], s, G) << (4 * (i & 7));
+  }
   return sc;
+}
+
+// the largest magnitude of 16
+__device__ __forceinline__ float amax16(const float* v) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
 }
 
 }  // namespace moe

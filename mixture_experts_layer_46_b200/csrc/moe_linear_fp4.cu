@@ -65,12 +65,39 @@ __device__ __forceinline__ void read32(const RowView& x, bool wide, int64_t row,
   }
 }
 
+// 16 neighbours of a row, as read32
+__device__ __forceinline__ void read16(const RowView& x, bool wide, int64_t row, int64_t c, float (&v)[16]) {
+  if (wide && x.dtype == MOE_BF16) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x.data) + row * x.s0 + c);
+    const uint4 a = p[0], b = p[1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else if (wide) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x.data) + row * x.s0 + c);
+    float4 r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[4 * i] = r[i].x; v[4 * i + 1] = r[i].y; v[4 * i + 2] = r[i].z; v[4 * i + 3] = r[i].w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = element(x, row, c + i);
+  }
+}
+
 // Codes (16 bytes) and scales (kNv: two e4m3 bytes; else one e8m0 byte) of 32 elements.
 template <bool kNv>
 __device__ __forceinline__ uint32_t quant32(const float (&v)[32], float G, uint32_t (&w)[4]) {
   if constexpr (kNv) {
     uint32_t a[2], b[2];
-    const uint32_t s0 = nv_quant16(v, G, a), s1 = nv_quant16(v + 16, G, b);
+    const float inv6 = 1.0f / (6.0f * G);
+    const uint32_t s0 = nv_quant16(v, amax16(v), G, inv6, a), s1 = nv_quant16(v + 16, amax16(v + 16), G, inv6, b);
     w[0] = a[0]; w[1] = a[1]; w[2] = b[0]; w[3] = b[1];
     return s0 | (s1 << 8);
   } else {
@@ -88,7 +115,7 @@ struct FpPrepare {
   int wide;
   int64_t T, K, N;
   int num_k, ntile, nh;   // k-steps, weight rows a tile, 128-row blocks a tile
-  int64_t x_items, w_items, x_blocks;
+  int64_t row_tiles, x_blocks, n_nt;  // 32-row tiles and blocks of x, tiles of the weight
   const float* x_global;
   uint8_t* codes;         // [T, num_k * 128]
   uint8_t* x_atoms;       // [128-row block][k-step][atom]
@@ -97,47 +124,102 @@ struct FpPrepare {
   uint8_t* w_atoms;       // [tile][k-step][atom][block]
 };
 
-template <bool kNv>
-__global__ void __launch_bounds__(256) fp4_prepare_kernel(const FpPrepare g) {
+// Blocks of 16 x 16 threads.  The first x_blocks walk over tiles of 32 rows x 256 elements of x,
+// a thread 16 neighbours of two rows, the next tile's on their way while the last ones are
+// quantised (blocks of one tile each spent their time starting up: 30 us instead of 16 at
+// T = 8192, K = 4096); the others place the weight's scales.  kFast: bf16, 16-byte loads.
+template <bool kNv, bool kFast>
+__global__ void __launch_bounds__(256, 4) fp4_prepare_kernel(const FpPrepare g) {
   constexpr int kAtoms = atoms_per_step<kNv>();
+  constexpr int kRows = 2;
   pdl_wait();
   pdl_launch_dependents();
   if (blockIdx.x < g.x_blocks) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= g.x_items) return;
-    const int per_row = g.num_k * 8;
-    const int64_t row = i / per_row;
-    const int c = static_cast<int>(i - row * per_row);  // group of 32
-    uint32_t sc = 0;
-    if (row < g.T && c * 32 < g.K) {
-      float v[32];
-      read32(g.x, g.wide, row, c * 32, v);
-      uint32_t w[4];
-      sc = quant32<kNv>(v, kNv ? *g.x_global : 1.0f, w);
-      *reinterpret_cast<uint4*>(g.codes + row * (static_cast<int64_t>(g.num_k) * 128) + c * 16) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float G = 1.0f, inv6 = 0.0f;
+    if (kNv) {
+      G = *g.x_global;
+      inv6 = 1.0f / (6.0f * G);
     }
-    const int per_step = kNv ? 16 : 8, q = kNv ? 2 * c : c;  // scale index in the row
-    const int step = q / per_step, in = q - step * per_step;
-    const int r = static_cast<int>(row & 127);
-    uint8_t* dst = g.x_atoms + (((row >> 7) * g.num_k + step) * kAtoms + (in >> 2)) * kAtomBytes +
-                   (r & 31) * 16 + (r >> 5) * 4 + (in & 3);
-    if (kNv)
-      *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sc);
-    else
-      *dst = static_cast<uint8_t>(sc);
+    // a block keeps its k-step and goes down the rows
+    const int step = static_cast<int>(blockIdx.x % g.num_k), c = step * 256 + tx * 16;
+    const int64_t first = blockIdx.x / g.num_k, stride = g.x_blocks / g.num_k;
+    const bool cols = c < g.K;
+    uint4 next[kRows][2];
+    auto fetch = [&](int64_t rb) {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const int64_t row = rb * (16 * kRows) + 16 * j + ty;
+        if (row < g.T && cols) {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.x.data) + row * g.x.s0 + c);
+          next[j][0] = p[0];
+          next[j][1] = p[1];
+        }
+      }
+    };
+    if (kFast) fetch(first);
+    for (int64_t rb = first; rb < g.row_tiles; rb += stride) {
+      uint4 cur[kRows][2];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        cur[j][0] = next[j][0];
+        cur[j][1] = next[j][1];
+      }
+      if (kFast) fetch(rb + stride);
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const int64_t row = rb * (16 * kRows) + 16 * j + ty;
+        uint32_t sc = 0;
+        if (row < g.T && cols) {
+          float v[16];
+          if constexpr (kFast) {
+            const uint32_t w[8] = {cur[j][0].x, cur[j][0].y, cur[j][0].z, cur[j][0].w,
+                                   cur[j][1].x, cur[j][1].y, cur[j][1].z, cur[j][1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              v[2 * i] = __uint_as_float(w[i] << 16);
+              v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+          } else {
+            read16(g.x, g.wide, row, c, v);
+          }
+          uint32_t w[2];
+          float amax = amax16(v);
+          if constexpr (kNv) {
+            sc = nv_quant16(v, amax, G, inv6, w);
+          } else {
+            // (K is a multiple of 32: both threads of a block are here)
+            amax = fmaxf(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30), amax, 1));
+            const int e = mx_scale_exp(amax);
+            const float f = exp2i_neg(e);
+            w[0] = cvt_e2m1x8(v, f);
+            w[1] = cvt_e2m1x8(v + 8, f);
+            sc = static_cast<uint32_t>(e + 127);
+          }
+          *reinterpret_cast<uint2*>(g.codes + row * (static_cast<int64_t>(g.num_k) * 128) + (c >> 1)) = make_uint2(w[0], w[1]);
+        }
+        // the threads of an atom's word (four blocks of 16, or of 32) hand their scales to the first
+        constexpr int kStep = kNv ? 1 : 2;  // threads a scale
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) sc |= __shfl_down_sync(0xffffffffu, sc, o * kStep) << (8 * o);
+        if (tx % (4 * kStep) == 0) {
+          const int r = static_cast<int>(row & 127);
+          *reinterpret_cast<uint32_t*>(g.x_atoms + (((row >> 7) * g.num_k + step) * kAtoms + tx / (4 * kStep)) * kAtomBytes +
+                                       (r & 31) * 16 + (r >> 5) * 4) = sc;
+        }
+      }
+    }
     return;
   }
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) - g.x_blocks) * 256 + threadIdx.x;
-  if (i >= g.w_items) return;
-  const int lane = static_cast<int>(i & 31);
-  int64_t atom = i >> 5;  // ((tile * num_k + step) * kAtoms + a) * nh + h
-  const int h = static_cast<int>(atom % g.nh);
-  int64_t rest = atom / g.nh;
-  const int a = static_cast<int>(rest % kAtoms);
-  rest /= kAtoms;
-  const int64_t tile = rest / g.num_k, step = rest - tile * g.num_k;
-  const int64_t q = (step * kAtoms + a) * 4, nq = g.K / (kNv ? 16 : 32);
+  const int64_t wb = static_cast<int64_t>(blockIdx.x) - g.x_blocks;
+  const int step = static_cast<int>(wb % g.num_k);
+  // [tile][atom][128-row block][lane] of this step
+  const int64_t i = wb / g.num_k * 256 + threadIdx.x;
+  const int lane = static_cast<int>(i & 31), log_nh = g.nh - 1;
+  const int h = static_cast<int>(i >> 5) & (g.nh - 1), a = static_cast<int>(i >> (5 + log_nh)) & (kAtoms - 1);
+  const int64_t tile = i >> (5 + log_nh + (kNv ? 2 : 1));
+  if (tile >= g.n_nt) return;
+  const int64_t q = (static_cast<int64_t>(step) * kAtoms + a) * 4, nq = g.K / (kNv ? 16 : 32);
   const bool whole = g.ws1 == 1 && q + 4 <= nq && (reinterpret_cast<uintptr_t>(g.w_sf) | g.ws0) % 4 == 0;
   uint32_t word[4];
 #pragma unroll
@@ -154,6 +236,7 @@ __global__ void __launch_bounds__(256) fp4_prepare_kernel(const FpPrepare g) {
         if (q + b < nq) word[j] |= static_cast<uint32_t>(p[b * g.ws1]) << (8 * b);
     }
   }
+  const int64_t atom = ((tile * g.num_k + step) * kAtoms + a) * g.nh + h;
   *reinterpret_cast<uint4*>(g.w_atoms + atom * kAtomBytes + lane * 16) = make_uint4(word[0], word[1], word[2], word[3]);
 }
 
@@ -699,9 +782,11 @@ cudaError_t launch_pair_path(const LinearFp4& a, const LinearFp4Plan& p, const C
   f.num_k = static_cast<int>(p.num_k);
   f.ntile = p.ntile;
   f.nh = p.nh;
-  f.x_items = p.n_mt * 2 * kTokRows * p.num_k * 8;
-  f.w_items = p.w_atoms * 32;
-  f.x_blocks = (f.x_items + 255) / 256;
+  f.n_nt = p.n_nt;
+  f.row_tiles = p.n_mt * 2 * kTokRows / 32;
+  int64_t per_step = 4 * num_sms / p.num_k;  // resident blocks
+  per_step = per_step < 1 ? 1 : per_step > f.row_tiles ? f.row_tiles : per_step;
+  f.x_blocks = per_step * p.num_k;
   f.x_global = a.x_global;
   f.codes = ws + p.codes_off;
   f.x_atoms = ws + p.x_off;
@@ -709,8 +794,10 @@ cudaError_t launch_pair_path(const LinearFp4& a, const LinearFp4Plan& p, const C
   f.ws0 = a.ws0;
   f.ws1 = a.ws1;
   f.w_atoms = ws + p.w_off;
-  const int64_t blocks = f.x_blocks + (f.w_items + 255) / 256;
-  cudaError_t rc = launch_pdl(fp4_prepare_kernel<kNv>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, f);
+  const int64_t w_blocks = (p.n_nt * atoms_per_step<kNv>() * p.nh * 32 + 255) / 256 * p.num_k;
+  const dim3 blocks(static_cast<unsigned>(f.x_blocks + w_blocks));
+  cudaError_t rc = a.wide && a.x.dtype == MOE_BF16 ? launch_pdl(fp4_prepare_kernel<kNv, true>, blocks, dim3(256), 0, st, f)
+                                                   : launch_pdl(fp4_prepare_kernel<kNv, false>, blocks, dim3(256), 0, st, f);
   if (rc != cudaSuccess) return rc;
   FpGemm g = {};
   g.T = a.T;
