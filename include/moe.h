@@ -500,7 +500,8 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
  * The layer around moe_forward (Liger-Kernel PR #1377, "Problems") at decoding sizes, from the
  * residual stream to the residual stream, for T <= MOE_LAYER_MAX_TOKENS tokens:
  *   xn     = x r pre_weight,  r_t = 1 / sqrt(mean x[t]^2 + eps)    (bf16 for the experts)
- *   logits = xn router^T (64-bit sums, xn not rounded), the k largest chosen, a tie going to
+ *   logits = xn router^T (xn not rounded; the sums carry their errors along, so that only terms
+ *            are rounded, to fp32 where pre_weight or router is f32), the k largest chosen, a tie going to
  *            the lower expert; topk_weights = softmax over all experts, or with renormalize = 1
  *            over the chosen ones; shared_expert = 1 adds column k: expert E, weight 1
  *   y      = moe_forward(xn, w13, w2, topk_ids, topk_weights)
@@ -514,8 +515,10 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
  *   topk_ids      [T, k + shared_expert] int32 or int64, topk_weights the same in f32; written
  *   workspace     moe_layer_decode_workspace_bytes (E and k with the shared expert counted in),
  *                 256-byte aligned; contents are scratch
- * bf16 weights and at most 32 slots: two kernels (three with post_norm); else the forward's kernels
- * between the first and the last.  Asynchronous on `stream`, no allocation.  T = 0 is a no-op. */
+ * Kernels: the way in (norm, router, choice); the experts, with bf16 weights and few tokens two
+ * kernels over their rows with xn and h in fp32, else the kernels of moe_forward; the gate and the
+ * residual are part of the last one, with post_norm = 1 or MXFP4 weights a kernel of their own.
+ * NaN logits rank below every number.  Asynchronous on `stream`, no allocation.  T = 0 is a no-op. */
 enum { MOE_LAYER_MAX_TOKENS = 32 };
 
 size_t moe_layer_decode_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int32_t wdtype);

@@ -414,7 +414,7 @@ moe_status_t moe_linear_fp4(const moe_tensor_t* x, const moe_tensor_t* weight, i
   return MOE_OK;
 }
 
-// [expert forward][normed rows bf16][the experts' rows: f32, or bf16 with MXFP4 weights]
+// [expert forward, or h of the kernels over rows][normed rows][the experts' rows: f32, or bf16 with MXFP4 weights]
 struct LayerWs {
   size_t xn, y, total;
 };
@@ -422,8 +422,9 @@ static bool layer_ws(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int3
   if (T < 0 || T > MOE_LAYER_MAX_TOKENS || H > kRouteMaxH) return false;
   const size_t fwd = moe_workspace_bytes(T > 0 ? T : 1, H, I, E, k, wdtype);
   if (fwd == 0) return false;
-  w->xn = round256(fwd);
-  w->y = w->xn + round256(static_cast<size_t>(T) * H * 2);
+  const size_t h = layer_by_rows(T, H, I, E, k) ? static_cast<size_t>(T) * k * I * 4 : 0;
+  w->xn = round256(fwd > h ? fwd : h);
+  w->y = w->xn + round256(static_cast<size_t>(T) * H * 4);
   w->total = w->y + round256(static_cast<size_t>(T) * H * 4);
   return true;
 }
@@ -474,7 +475,8 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
   MOE_TRY(api_device(&sms, nullptr));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  r.wide = r.router.dtype == MOE_BF16 && r.w.dtype == MOE_BF16 && H % 8 == 0 && wide_ok(r.router);
+  r.wide = r.router.dtype == MOE_BF16 && H % 8 == 0 && wide_ok(r.router);
+  r.x_wide = r.w.dtype == MOE_BF16 && H % 8 == 0 && wide_ok(r.x) && wide_ok(r.w);
   r.T = T;
   r.H = static_cast<int>(H);
   r.E = static_cast<int>(E);
@@ -482,7 +484,9 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
   r.renorm = renormalize;
   r.shared = shared_expert;
   r.eps = eps;
+  const bool by_rows = wd == MOE_BF16 && layer_by_rows(T, H, I, E + shared_expert, k + shared_expert);
   r.xn = reinterpret_cast<__nv_bfloat16*>(ws + L.xn);
+  r.xn32 = by_rows ? reinterpret_cast<float*>(ws + L.xn) : nullptr;
   r.ids = View2{topk_ids->data, topk_ids->strides[0], topk_ids->strides[1], topk_ids->dtype};
   r.wts = View2{topk_weights->data, topk_weights->strides[0], topk_weights->strides[1], topk_weights->dtype};
   const cudaError_t rc = launch_route(r, st);
@@ -511,8 +515,37 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
     f.mode = kFinishRows;
     f.y32 = reinterpret_cast<float*>(ws + L.y);
   }
-  MOE_TRY(api_forward(&xn, w13, w2, topk_ids, topk_weights, after ? &y : out, workspace, L.xn, st, f));
-  launches += api_launches();
+  if (by_rows) {
+    LayerRows a = {};
+    a.xn = r.xn32;
+    a.h = reinterpret_cast<float*>(ws);
+    a.ids = r.ids;
+    a.wts = r.wts;
+    a.T = static_cast<int>(T);
+    a.k = k + shared_expert;
+    a.H = static_cast<int>(H);
+    a.I = static_cast<int>(I);
+    a.E = E + shared_expert;
+    a.gate = static_cast<const __nv_bfloat16*>(w13->gate.data);
+    a.up = static_cast<const __nv_bfloat16*>(w13->up.data);
+    a.w2 = static_cast<const __nv_bfloat16*>(w2->data);
+    a.gs0 = w13->gate.strides[0];
+    a.gs1 = w13->gate.strides[1];
+    a.us0 = w13->up.strides[0];
+    a.us1 = w13->up.strides[1];
+    a.ws0 = w2->strides[0];
+    a.ws1 = w2->strides[1];
+    a.out = static_cast<__nv_bfloat16*>(out->data);
+    a.os0 = out->strides[0];
+    a.os1 = out->strides[1];
+    a.finish = f;
+    const cudaError_t rr = launch_layer_rows(a, sms, st);
+    if (rr != cudaSuccess) return api_cuda_fail(rr, "layer_decode rows");
+    launches += 2;
+  } else {
+    MOE_TRY(api_forward(&xn, w13, w2, topk_ids, topk_weights, after ? &y : out, workspace, L.xn, st, f));
+    launches += api_launches();
+  }
   if (after) {
     if (f.mode == kFinishRows) y.dtype = MOE_F32;
     MOE_TRY(moe_norm_after(&y, x, post_weight, gate, gate_act, post_norm, residual_scale, eps, out, nullptr, nullptr,

@@ -119,13 +119,32 @@ constexpr int64_t kRouteMaxH = 16384, kRouteMaxE = 1024;
 struct Route {
   RowView x, w, router;  // w: no data = ones; router [E, H]
   int wide;              // router: bf16, 16-byte rows
+  int x_wide;            // x and w likewise
   int64_t T;
   int H, E, k, renorm, shared;
   float eps;
-  __nv_bfloat16* xn;     // [T, H]
+  __nv_bfloat16* xn;     // [T, H], or
+  float* xn32;           // the same unrounded
   View2 ids, wts;
 };
 cudaError_t launch_route(const Route& g, cudaStream_t st);
+
+// ---- a layer's experts for a few tokens (moe_layer_rows.cu) --------------
+
+struct LayerRows {
+  const float* xn;  // [T, H]
+  float* h;         // [T k, I]
+  View2 ids, wts;
+  int T, k, H, I;
+  int64_t E;        // the shared expert counted in
+  const __nv_bfloat16 *gate, *up, *w2;  // strides in elements, inner stride 1, 16-byte rows
+  int64_t gs0, gs1, us0, us1, ws0, ws1;
+  __nv_bfloat16* out;
+  int64_t os0, os1;
+  Finish finish;    // kFinishRows or kFinishGate
+};
+bool layer_by_rows(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);
+cudaError_t launch_layer_rows(const LayerRows& a, int num_sms, cudaStream_t st);
 
 // ---- 4-bit linear layer (moe_linear_fp4.cu) -----------------------------------
 
