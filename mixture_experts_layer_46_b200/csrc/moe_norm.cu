@@ -21,6 +21,7 @@
 // every blockDim-th element through the strides, which keeps a warp's accesses together.
 // Arithmetic is fp32 throughout; each output is rounded once, to its own type.
 #include <atomic>
+#include <initializer_list>
 
 #include "../../include/moe.h"
 #include "moe_block.h"
@@ -34,8 +35,22 @@ struct Vec8 {
   float v[8];
 };
 
-// How a kernel reads its row tensors: through the strides, 16 bytes a load, or from the ring.
-enum { kStrided = 0, kWide = 1, kRing = 2 };
+// How a kernel reads its row tensors: through the strides, 16 bytes a load, or from the ring.  The
+// ring comes in three forms: any types, all bf16, and a float stream around a bf16 block; known
+// types halve the instructions, which bound the ring otherwise (T=16384 H=4096 bf16, after + next:
+// 37 a element with types as arguments).
+enum { kStrided = 0, kWide = 1, kRing = 2, kRingBf16 = 3, kRingF32 = 4 };
+constexpr bool is_ring(int mode) { return mode >= kRing; }
+// the type of a tensor of the residual stream (x, out, their gradients), and of the block's (y, the
+// normed rows, the gate)
+template <int kMode>
+__device__ __forceinline__ int32_t stream_type(const RowView& t) {
+  return kMode == kRingBf16 ? MOE_BF16 : kMode == kRingF32 ? MOE_F32 : t.dtype;
+}
+template <int kMode>
+__device__ __forceinline__ int32_t block_type(const RowView& t) {
+  return kMode >= kRingBf16 ? MOE_BF16 : t.dtype;
+}
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -67,8 +82,8 @@ __device__ __forceinline__ void read8(const void* row, int c, int32_t dtype, Raw
   }
 }
 
-__device__ __forceinline__ const char* row_ptr(const RowView& t, int64_t row) {
-  return static_cast<const char*>(t.data) + row * t.s0 * (t.dtype == MOE_F32 ? 4 : 2);
+__device__ __forceinline__ const char* row_ptr(const RowView& t, int64_t row, int32_t dtype) {
+  return static_cast<const char*>(t.data) + row * t.s0 * (dtype == MOE_F32 ? 4 : 2);
 }
 
 __device__ __forceinline__ void zero8(Raw8& o) {
@@ -78,7 +93,7 @@ __device__ __forceinline__ void zero8(Raw8& o) {
 
 template <int kMode>
 __device__ __forceinline__ void load8(const RowView& t, int64_t row, int slot, int H, Raw8& o) {
-  const char* base = row_ptr(t, row);
+  const char* base = row_ptr(t, row, t.dtype);
   zero8(o);
   if (kMode != kStrided) {
     const int c = col_of<true>(slot, 0);
@@ -118,12 +133,12 @@ __device__ __forceinline__ Vec8 unpack8(const Raw8& r, int32_t dtype) {
 }
 
 template <int kMode>
-__device__ __forceinline__ void store8(const RowView& t, int64_t row, int slot, int H, const Vec8& o) {
-  char* base = const_cast<char*>(row_ptr(t, row));
+__device__ __forceinline__ void store8(const RowView& t, int32_t dtype, int64_t row, int slot, int H, const Vec8& o) {
+  char* base = const_cast<char*>(row_ptr(t, row, dtype));
   if (kMode != kStrided) {
     const int c = col_of<true>(slot, 0);
     if (c >= H) return;
-    if (t.dtype == MOE_F32) {
+    if (dtype == MOE_F32) {
       float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + c);
       p[0] = make_float4(o.v[0], o.v[1], o.v[2], o.v[3]);
       p[1] = make_float4(o.v[4], o.v[5], o.v[6], o.v[7]);
@@ -137,7 +152,7 @@ __device__ __forceinline__ void store8(const RowView& t, int64_t row, int slot, 
     for (int i = 0; i < 8; ++i) {
       const int c = col_of<false>(slot, i);
       if (c >= H) continue;
-      if (t.dtype == MOE_F32)
+      if (dtype == MOE_F32)
         reinterpret_cast<float*>(base)[c * t.s1] = o.v[i];
       else
         reinterpret_cast<__nv_bfloat16*>(base)[c * t.s1] = __float2bfloat16_rn(o.v[i]);
@@ -171,7 +186,7 @@ struct Ring {
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                 smem_u32(smem + s * a.stage_bytes + a.off[i])),
-            "l"(row_ptr(a.in[i], t)), "r"(a.bytes[i]), "r"(smem_u32(&full[s]))
+            "l"(row_ptr(a.in[i], t, a.in[i].dtype)), "r"(a.bytes[i]), "r"(smem_u32(&full[s]))
             : "memory");
   }
   __device__ __forceinline__ void start(int64_t T) {
@@ -190,10 +205,10 @@ struct Ring {
   __device__ __forceinline__ void wait() {
     if (ok && !mbar_wait(&full[stage], phase, threadIdx.x == 0 ? a.err : nullptr)) ok = false;
   }
-  __device__ __forceinline__ void read(int i, int slot, int H, Raw8& o) const {
+  __device__ __forceinline__ void read(int i, int32_t dtype, int slot, int H, Raw8& o) const {
     const int c = col_of<true>(slot, 0);
     zero8(o);
-    if (c < H) read8(smem + stage * a.stage_bytes + a.off[i], c, a.in[i].dtype, o);
+    if (c < H) read8(smem + stage * a.stage_bytes + a.off[i], c, dtype, o);
   }
   // every thread has read its part of row t: the stage takes the row `stages` rounds on
   __device__ __forceinline__ void next(int64_t t, int64_t T) {
@@ -206,9 +221,9 @@ struct Ring {
 
 // row tensor i of the kernel: from the ring, or from memory
 template <int kMode>
-__device__ __forceinline__ void input8(const Ring& ring, int i, int64_t row, int slot, int H, Raw8& o) {
-  if (kMode == kRing)
-    ring.read(i, slot, H, o);
+__device__ __forceinline__ void input8(const Ring& ring, int i, int32_t dtype, int64_t row, int slot, int H, Raw8& o) {
+  if (is_ring(kMode))
+    ring.read(i, dtype, slot, H, o);
   else
     load8<kMode>(ring.a.in[i], row, slot, H, o);
 }
@@ -218,9 +233,10 @@ template <int kMode>
 __device__ __forceinline__ Vec8 load_weight(const RowView& t, int slot, int H) {
   Vec8 o;
   if (t.data) {
+    constexpr int kHow = kMode == kStrided ? kStrided : kWide;
     Raw8 r;
-    load8<kMode>(t, 0, slot, H, r);
-    o = unpack8<kMode>(r, t.dtype);
+    load8<kHow>(t, 0, slot, H, r);
+    o = unpack8<kHow>(r, t.dtype);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) o.v[i] = 1.0f;
@@ -260,7 +276,9 @@ __device__ __forceinline__ void gate_slopes(Vec8& g, int act) {
 }
 
 // Sum of v over the block; every thread gets it.  One barrier a call: two scratch rows are
-// used in turn, and a row is written again only after the other one's barrier.
+// used in turn, and a row is written again only after the other one's barrier.  (Up to eight
+// warps every thread adds their sums itself: two broadcast loads and no second tree.)
+template <int kMaxThreads>
 __device__ __forceinline__ float block_sum(float v, float (*scratch)[32], int& turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -270,14 +288,28 @@ __device__ __forceinline__ float block_sum(float v, float (*scratch)[32], int& t
   turn ^= 1;
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
+  if (kMaxThreads <= 256) {
+    const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+    const float e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float r = e[0] + e[1];
+#pragma unroll
+    for (int i = 2; i < 8; ++i) r += i < warps ? e[i] : 0.0f;
+    return r;
+  }
   float r = static_cast<int>(threadIdx.x & 31) < warps ? s[threadIdx.x & 31] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
   return r;
 }
 
-__device__ __forceinline__ float inv_root(float sum, int H, float eps) {
-  return 1.0f / sqrtf(sum / static_cast<float>(H) + eps);
+// 1 / sqrt(sum / H + eps): the fast root (2 ulp) and one step of Newton's (a correctly rounded
+// root and two divisions were a fifth of a row's instructions).  A zero, infinite or tiny argument
+// keeps the fast root's value, which the step would turn into NaN.
+__device__ __forceinline__ float inv_root(float sum, float inv_h, float eps) {
+  const float a = fmaf(sum, inv_h, eps), y = rsqrtf(a);
+  const float e = fmaf(-a * y, y, 1.0f);
+  const float r = fmaf(0.5f * y, e, y);
+  return a > 1e-30f && a < 1e30f ? r : y;
 }
 
 // Threads of resident blocks on an SM: 80 and 128 registers a thread, what the kernels need
@@ -291,38 +323,40 @@ constexpr int forward_threads(bool ring) { return ring ? kRingThreads : kDirectT
 // ---------------------------------------------------------------- forward
 
 template <int kVec, int kMode, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(kMode == kRing), kMaxThreads))
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(is_ring(kMode)), kMaxThreads))
     norm_before_kernel(const NormBefore g) {
   extern __shared__ __align__(128) char smem[];
-  __shared__ float scratch[2][32];
+  __shared__ __align__(16) float scratch[2][32];
   pdl_wait();
   pdl_launch_dependents();
   int turn = 0;
+  const float inv_h = 1.0f / static_cast<float>(g.H);
+  const int32_t xt = stream_type<kMode>(g.ring.in[0]);
   Ring ring(g.ring, smem);
-  if (kMode == kRing) ring.start(g.T);
+  if (is_ring(kMode)) ring.start(g.T);
   Vec8 w[kVec];
 #pragma unroll
   for (int v = 0; v < kVec; ++v) w[v] = load_weight<kMode>(g.w, v, g.H);
   for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    if (kMode == kRing) ring.wait();
+    if (is_ring(kMode)) ring.wait();
     Raw8 raw[kVec];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) input8<kMode>(ring, 0, t, v, g.H, raw[v]);
-    if (kMode == kRing) ring.next(t, g.T);
+    for (int v = 0; v < kVec; ++v) input8<kMode>(ring, 0, xt, t, v, g.H, raw[v]);
+    if (is_ring(kMode)) ring.next(t, g.T);
     Vec8 x[kVec];
     float ss = 0.0f;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      x[v] = unpack8<kMode>(raw[v], g.ring.in[0].dtype);
+      x[v] = unpack8<kMode>(raw[v], xt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss += x[v].v[i] * x[v].v[i];
     }
-    const float r = inv_root(block_sum(ss, scratch, turn), g.H, g.eps);
+    const float r = inv_root(block_sum<kMaxThreads>(ss, scratch, turn), inv_h, g.eps);
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[v].v[i] *= r * w[v].v[i];
-      store8<kMode>(g.out, t, v, g.H, x[v]);
+      store8<kMode>(g.out, block_type<kMode>(g.out), t, v, g.H, x[v]);
     }
     if (g.rstd && threadIdx.x == 0) g.rstd[t * g.rstd_s] = r;
   }
@@ -332,15 +366,17 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(kMode 
 // kept in registers unrounded between the two reductions, the weights (a per-channel gate
 // multiplied in) for all of the block's rows.
 template <int kVec, int kMode, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(kMode == kRing), kMaxThreads))
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(is_ring(kMode)), kMaxThreads))
     norm_after_kernel(const NormAfter g) {
   extern __shared__ __align__(128) char smem[];
-  __shared__ float scratch[2][32];
+  __shared__ __align__(16) float scratch[2][32];
   pdl_wait();
   pdl_launch_dependents();
   int turn = 0;
+  const float inv_h = 1.0f / static_cast<float>(g.H);
+  const int32_t yt = block_type<kMode>(g.ring.in[0]), xt = stream_type<kMode>(g.ring.in[1]), gtt = block_type<kMode>(g.ring.in[2]);
   Ring ring(g.ring, smem);
-  if (kMode == kRing) ring.start(g.T);
+  if (is_ring(kMode)) ring.start(g.T);
   const bool have_x = g.ring.in[1].data != nullptr;
   const bool gate_full = g.ring.in[2].data != nullptr;
   const bool want_next = g.nxt.data || g.next_rstd;
@@ -356,24 +392,28 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(kMode 
       for (int i = 0; i < 8; ++i) w[v].v[i] *= c.v[i];
     }
   }
+  const bool gate_row = g.gate_mode == kGateToken || g.gate_mode == kGateOne;
+  float gate_next = gate_row && blockIdx.x < g.T ? scalar_at(g.gate, blockIdx.x * g.gate.s0) : 0.0f;
   for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    if (kMode == kRing) ring.wait();
+    const float gate_now = gate_next;  // read a row ahead
+    if (gate_row && t + gridDim.x < g.T) gate_next = scalar_at(g.gate, (t + gridDim.x) * g.gate.s0);
+    if (is_ring(kMode)) ring.wait();
     Raw8 y[kVec], x[kVec], gt[kVec];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) input8<kMode>(ring, 0, t, v, g.H, y[v]);
-    if (kMode != kRing) {  // (the ring's rows wait in shared memory until they are needed)
+    for (int v = 0; v < kVec; ++v) input8<kMode>(ring, 0, yt, t, v, g.H, y[v]);
+    if (!is_ring(kMode)) {  // (the ring's rows wait in shared memory until they are needed)
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
-        if (have_x) input8<kMode>(ring, 1, t, v, g.H, x[v]);
-        if (gate_full) input8<kMode>(ring, 2, t, v, g.H, gt[v]);
+        if (have_x) input8<kMode>(ring, 1, xt, t, v, g.H, x[v]);
+        if (gate_full) input8<kMode>(ring, 2, gtt, t, v, g.H, gt[v]);
       }
     }
     // a gate of one number a row (or one in all) is part of the row's factor
     float f = 1.0f;
-    if (g.gate_mode == kGateToken || g.gate_mode == kGateOne) f = gate_value(scalar_at(g.gate, t * g.gate.s0), g.act);
+    if (gate_row) f = gate_value(gate_now, g.act);
     Vec8 o[kVec];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) o[v] = unpack8<kMode>(y[v], g.ring.in[0].dtype);
+    for (int v = 0; v < kVec; ++v) o[v] = unpack8<kMode>(y[v], yt);
     float r = 1.0f;
     if (g.normalize) {
       float ss = 0.0f;
@@ -381,7 +421,7 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(kMode 
       for (int v = 0; v < kVec; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += o[v].v[i] * o[v].v[i];
-      r = inv_root(block_sum(ss, scratch, turn), g.H, g.eps);
+      r = inv_root(block_sum<kMaxThreads>(ss, scratch, turn), inv_h, g.eps);
     }
     if (g.rstd && threadIdx.x == 0) g.rstd[t * g.rstd_s] = r;
     f *= r;
@@ -391,32 +431,32 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(kMode 
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[v].v[i] *= f * w[v].v[i];
       if (gate_full) {
-        if (kMode == kRing) input8<kMode>(ring, 2, t, v, g.H, gt[v]);
-        Vec8 c = unpack8<kMode>(gt[v], g.ring.in[2].dtype);
+        if (is_ring(kMode)) input8<kMode>(ring, 2, gtt, t, v, g.H, gt[v]);
+        Vec8 c = unpack8<kMode>(gt[v], gtt);
         gate_values(c, g.act);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[v].v[i] *= c.v[i];
       }
       if (have_x) {
-        if (kMode == kRing) input8<kMode>(ring, 1, t, v, g.H, x[v]);
-        const Vec8 c = unpack8<kMode>(x[v], g.ring.in[1].dtype);
+        if (is_ring(kMode)) input8<kMode>(ring, 1, xt, t, v, g.H, x[v]);
+        const Vec8 c = unpack8<kMode>(x[v], xt);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[v].v[i] += g.alpha * c.v[i];
       }
-      store8<kMode>(g.out, t, v, g.H, o[v]);
+      store8<kMode>(g.out, stream_type<kMode>(g.out), t, v, g.H, o[v]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss += o[v].v[i] * o[v].v[i];
     }
-    if (kMode == kRing) ring.next(t, g.T);
+    if (is_ring(kMode)) ring.next(t, g.T);
     if (want_next) {
-      const float rn = inv_root(block_sum(ss, scratch, turn), g.H, g.eps);
+      const float rn = inv_root(block_sum<kMaxThreads>(ss, scratch, turn), inv_h, g.eps);
       if (g.next_rstd && threadIdx.x == 0) g.next_rstd[t * g.next_rstd_s] = rn;
       if (g.nxt.data) {
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[v].v[i] *= rn * wn[v].v[i];
-          store8<kMode>(g.nxt, t, v, g.H, o[v]);
+          store8<kMode>(g.nxt, block_type<kMode>(g.nxt), t, v, g.H, o[v]);
         }
       }
     }
@@ -434,19 +474,21 @@ __device__ __forceinline__ void store_partial(float* part, int H, const Vec8 (&a
   p.s1 = 1;
   p.dtype = MOE_F32;
 #pragma unroll
-  for (int v = 0; v < kVec; ++v) store8<kMode>(p, blockIdx.x, v, H, acc[v]);
+  for (int v = 0; v < kVec; ++v) store8<kMode == kStrided ? kStrided : kWide>(p, MOE_F32, blockIdx.x, v, H, acc[v]);
 }
 
 template <int kVec, int kMode, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMaxThreads))
     norm_before_backward_kernel(const NormBeforeBackward g) {
   extern __shared__ __align__(128) char smem[];
-  __shared__ float scratch[2][32];
+  __shared__ __align__(16) float scratch[2][32];
   pdl_wait();
   pdl_launch_dependents();
   int turn = 0;
+  const float inv_h = 1.0f / static_cast<float>(g.H);
+  const int32_t dt = block_type<kMode>(g.ring.in[0]), xt = stream_type<kMode>(g.ring.in[1]), rt = stream_type<kMode>(g.ring.in[2]);
   Ring ring(g.ring, smem);
-  if (kMode == kRing) ring.start(g.T);
+  if (is_ring(kMode)) ring.start(g.T);
   const bool have_res = g.ring.in[2].data != nullptr;
   Vec8 dw[kVec], w[kVec];
 #pragma unroll
@@ -455,22 +497,24 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v].v[i] = 0.0f;
   }
+  float r_next = blockIdx.x < g.T ? g.rstd[blockIdx.x * g.rstd_s] : 0.0f;
   for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    const float r = g.rstd[t * g.rstd_s];
-    if (kMode == kRing) ring.wait();
+    const float r = r_next;
+    if (t + gridDim.x < g.T) r_next = g.rstd[(t + gridDim.x) * g.rstd_s];
+    if (is_ring(kMode)) ring.wait();
     Raw8 rd[kVec], rx[kVec], res[kVec];
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      input8<kMode>(ring, 0, t, v, g.H, rd[v]);
-      input8<kMode>(ring, 1, t, v, g.H, rx[v]);
-      if (kMode != kRing && have_res) input8<kMode>(ring, 2, t, v, g.H, res[v]);
+      input8<kMode>(ring, 0, dt, t, v, g.H, rd[v]);
+      input8<kMode>(ring, 1, xt, t, v, g.H, rx[v]);
+      if (!is_ring(kMode) && have_res) input8<kMode>(ring, 2, rt, t, v, g.H, res[v]);
     }
     Vec8 p[kVec], x[kVec];
     float dot = 0.0f;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      p[v] = unpack8<kMode>(rd[v], g.ring.in[0].dtype);
-      x[v] = unpack8<kMode>(rx[v], g.ring.in[1].dtype);
+      p[v] = unpack8<kMode>(rd[v], dt);
+      x[v] = unpack8<kMode>(rx[v], xt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[v].v[i] *= r;
@@ -479,20 +523,20 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
         dot += p[v].v[i] * x[v].v[i];
       }
     }
-    const float c = block_sum(dot, scratch, turn) / static_cast<float>(g.H);
+    const float c = block_sum<kMaxThreads>(dot, scratch, turn) * inv_h;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[v].v[i] = r * (p[v].v[i] - x[v].v[i] * c);
       if (have_res) {
-        if (kMode == kRing) input8<kMode>(ring, 2, t, v, g.H, res[v]);
-        const Vec8 d = unpack8<kMode>(res[v], g.ring.in[2].dtype);
+        if (is_ring(kMode)) input8<kMode>(ring, 2, rt, t, v, g.H, res[v]);
+        const Vec8 d = unpack8<kMode>(res[v], rt);
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[v].v[i] += g.alpha * d.v[i];
       }
-      store8<kMode>(g.dx, t, v, g.H, p[v]);
+      store8<kMode>(g.dx, stream_type<kMode>(g.dx), t, v, g.H, p[v]);
     }
-    if (kMode == kRing) ring.next(t, g.T);
+    if (is_ring(kMode)) ring.next(t, g.T);
   }
   if (g.part) store_partial<kVec, kMode>(g.part, g.H, dw);
 }
@@ -501,12 +545,14 @@ template <int kVec, int kMode, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMaxThreads))
     norm_after_backward_kernel(const NormAfterBackward g) {
   extern __shared__ __align__(128) char smem[];
-  __shared__ float scratch[2][32];
+  __shared__ __align__(16) float scratch[2][32];
   pdl_wait();
   pdl_launch_dependents();
   int turn = 0;
+  const float inv_h = 1.0f / static_cast<float>(g.H);
+  const int32_t dt = stream_type<kMode>(g.ring.in[0]), yt = block_type<kMode>(g.ring.in[1]), gtt = block_type<kMode>(g.ring.in[2]);
   Ring ring(g.ring, smem);
-  if (kMode == kRing) ring.start(g.T);
+  if (is_ring(kMode)) ring.start(g.T);
   const bool gate_full = g.gate_mode == kGateFull;
   const bool gate_col = g.gate_mode == kGateChannel;
   const bool gate_row = g.gate_mode == kGateToken || g.gate_mode == kGateOne;
@@ -524,39 +570,47 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v].v[i] = 0.0f;
   }
+  // a row's numbers are read a row ahead
+  float r_next = 1.0f, gate_next = 0.0f;
+  auto fetch_row = [&](int64_t t) {
+    if (t >= g.T) return;
+    if (g.normalize) r_next = g.rstd[t * g.rstd_s];
+    if (gate_row) gate_next = scalar_at(g.gate, t * g.gate.s0);
+  };
+  fetch_row(blockIdx.x);
   for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
-    const float r = g.normalize ? g.rstd[t * g.rstd_s] : 1.0f;
+    const float r = r_next, raw = gate_next;
+    fetch_row(t + gridDim.x);
     float rowv = 1.0f, rowslope = 1.0f;
     if (gate_row) {
-      const float raw = scalar_at(g.gate, t * g.gate.s0);
       rowv = gate_value(raw, g.act);
       rowslope = gate_slope(raw, g.act);
     }
-    if (kMode == kRing) ring.wait();
+    if (is_ring(kMode)) ring.wait();
     Raw8 rd[kVec], ry[kVec], rg[kVec];
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      input8<kMode>(ring, 0, t, v, g.H, rd[v]);
-      input8<kMode>(ring, 1, t, v, g.H, ry[v]);
-      if (kMode != kRing && gate_full) input8<kMode>(ring, 2, t, v, g.H, rg[v]);
+      input8<kMode>(ring, 0, dt, t, v, g.H, rd[v]);
+      input8<kMode>(ring, 1, yt, t, v, g.H, ry[v]);
+      if (!is_ring(kMode) && gate_full) input8<kMode>(ring, 2, gtt, t, v, g.H, rg[v]);
     }
     Vec8 d[kVec], y[kVec];
     float dot = 0.0f, gsum = 0.0f;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      d[v] = unpack8<kMode>(rd[v], g.ring.in[0].dtype);
-      y[v] = unpack8<kMode>(ry[v], g.ring.in[1].dtype);
+      d[v] = unpack8<kMode>(rd[v], dt);
+      y[v] = unpack8<kMode>(ry[v], yt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[v].v[i] *= r;
       if (gate_full) {
-        if (kMode == kRing) input8<kMode>(ring, 2, t, v, g.H, rg[v]);
-        Vec8 c = unpack8<kMode>(rg[v], g.ring.in[2].dtype);
+        if (is_ring(kMode)) input8<kMode>(ring, 2, gtt, t, v, g.H, rg[v]);
+        Vec8 c = unpack8<kMode>(rg[v], gtt);
         if (g.dgate.data) {
           Vec8 e = c;
           gate_slopes(e, g.act);
 #pragma unroll
           for (int i = 0; i < 8; ++i) e.v[i] *= d[v].v[i] * y[v].v[i] * w[v].v[i];
-          store8<kMode>(g.dgate, t, v, g.H, e);
+          store8<kMode>(g.dgate, g.dgate.dtype, t, v, g.H, e);
         }
         gate_values(c, g.act);
 #pragma unroll
@@ -573,11 +627,11 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
         dot += d[v].v[i] * y[v].v[i];
       }
     }
-    if (kMode == kRing) ring.next(t, g.T);
+    if (is_ring(kMode)) ring.next(t, g.T);
     float c = 0.0f;
-    if (g.normalize) c = block_sum(dot, scratch, turn) / static_cast<float>(g.H);
+    if (g.normalize) c = block_sum<kMaxThreads>(dot, scratch, turn) * inv_h;
     if (gate_row && g.dgate.data) {
-      const float s = block_sum(gsum, scratch, turn);
+      const float s = block_sum<kMaxThreads>(gsum, scratch, turn);
       if (g.gate_mode == kGateOne) {
         dall += s;
       } else if (threadIdx.x == 0) {
@@ -593,7 +647,7 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
     for (int v = 0; v < kVec; ++v) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[v].v[i] = r * (d[v].v[i] - y[v].v[i] * c);
-      store8<kMode>(g.dy, t, v, g.H, y[v]);
+      store8<kMode>(g.dy, block_type<kMode>(g.dy), t, v, g.H, y[v]);
     }
   }
   if (g.part) store_partial<kVec, kMode>(g.part, g.H, dw);
@@ -621,7 +675,16 @@ __global__ void __launch_bounds__(32 * kStrips) column_sum_kernel(const ColumnSu
   if (one && blockIdx.x != 0) return;
   float s = 0.0f;
   if (c < n && part)
-    for (int row = threadIdx.y; row < g.rows; row += kStrips) s += part[static_cast<int64_t>(row) * n + c];
+    for (int base = threadIdx.y; base < g.rows; base += 10 * kStrips) {
+      float v[10];  // (two blocks an SM leave up to 320 rows: one trip to memory)
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        const int row = base + i * kStrips;
+        v[i] = row < g.rows ? part[static_cast<int64_t>(row) * n + c] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 10; ++i) s += v[i];
+    }
   acc[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || c >= n) return;
@@ -704,13 +767,26 @@ cudaError_t launch_rows(const Args& g, int threads, int64_t grid, int smem, cuda
   ((s).threads <= 256   ? launch_rows<K<V, M, 256>>(g, (s).threads, grid, smem, st)                   \
    : (s).threads <= 512 ? launch_rows<K<2, M, 512>>(g, (s).threads, grid, smem, st)                   \
                         : launch_rows<K<2, M, 1024>>(g, (s).threads, grid, smem, st))
-#define MOE_NORM_LAUNCH(K, g, wide, s, grid, smem, st)                                                \
-  ((s).vec == 1 ? (!(wide)     ? MOE_NORM_MODE(K, 1, kStrided, g, s, grid, 0, st)                     \
-                   : (smem) == 0 ? MOE_NORM_MODE(K, 1, kWide, g, s, grid, 0, st)                      \
-                                 : MOE_NORM_MODE(K, 1, kRing, g, s, grid, smem, st))                  \
-                : (!(wide)     ? MOE_NORM_MODE(K, 2, kStrided, g, s, grid, 0, st)                     \
-                   : (smem) == 0 ? MOE_NORM_MODE(K, 2, kWide, g, s, grid, 0, st)                      \
-                                 : MOE_NORM_MODE(K, 2, kRing, g, s, grid, smem, st)))
+#define MOE_NORM_VEC(K, V, mode, g, s, grid, smem, st)                                                \
+  ((mode) == kStrided    ? MOE_NORM_MODE(K, V, kStrided, g, s, grid, 0, st)                           \
+   : (mode) == kWide     ? MOE_NORM_MODE(K, V, kWide, g, s, grid, 0, st)                              \
+   : (mode) == kRingBf16 ? MOE_NORM_MODE(K, V, kRingBf16, g, s, grid, smem, st)                       \
+   : (mode) == kRingF32  ? MOE_NORM_MODE(K, V, kRingF32, g, s, grid, smem, st)                        \
+                         : MOE_NORM_MODE(K, V, kRing, g, s, grid, smem, st))
+#define MOE_NORM_LAUNCH(K, g, mode, s, grid, smem, st)                                                \
+  ((s).vec == 1 ? MOE_NORM_VEC(K, 1, mode, g, s, grid, smem, st) : MOE_NORM_VEC(K, 2, mode, g, s, grid, smem, st))
+
+// the ring's form from the types of the stream's and the block's tensors (absent ones do not count)
+int mode_of(bool wide, int smem, std::initializer_list<const RowView*> stream, std::initializer_list<const RowView*> block) {
+  if (!wide) return kStrided;
+  if (smem == 0) return kWide;
+  bool b16 = true, f32 = true;
+  for (const RowView* v : stream)
+    if (v->data) (v->dtype == MOE_F32 ? b16 : f32) = false;
+  for (const RowView* v : block)
+    if (v->data && v->dtype != MOE_BF16) b16 = f32 = false;
+  return b16 ? kRingBf16 : f32 ? kRingF32 : kRing;
+}
 
 template <typename Args>
 int prepare(Args* g, const Shape& s, bool wide, int threads_per_sm, int64_t grid) {
@@ -728,28 +804,32 @@ cudaError_t launch_norm_before(NormBefore g, bool wide, int num_sms, cudaStream_
   const Shape s = shape_of(g.H);
   const int64_t grid = blocks_of(g.T, s.threads, num_sms, forward_threads(wide));
   const int smem = prepare(&g, s, wide, forward_threads(wide), grid);
-  return MOE_NORM_LAUNCH(norm_before_kernel, g, wide, s, grid, smem, st);
+  const int mode = mode_of(wide, smem, {&g.ring.in[0]}, {&g.out});
+  return MOE_NORM_LAUNCH(norm_before_kernel, g, mode, s, grid, smem, st);
 }
 
 cudaError_t launch_norm_after(NormAfter g, bool wide, int num_sms, cudaStream_t st) {
   const Shape s = shape_of(g.H);
   const int64_t grid = blocks_of(g.T, s.threads, num_sms, forward_threads(wide));
   const int smem = prepare(&g, s, wide, forward_threads(wide), grid);
-  return MOE_NORM_LAUNCH(norm_after_kernel, g, wide, s, grid, smem, st);
+  const int mode = mode_of(wide, smem, {&g.ring.in[1], &g.out}, {&g.ring.in[0], &g.ring.in[2], &g.nxt});
+  return MOE_NORM_LAUNCH(norm_after_kernel, g, mode, s, grid, smem, st);
 }
 
 cudaError_t launch_norm_before_backward(NormBeforeBackward g, bool wide, int num_sms, cudaStream_t st) {
   const Shape s = shape_of(g.H);
   const int64_t grid = norm_backward_rows(g.T, g.H, num_sms);
   const int smem = prepare(&g, s, wide, kBackwardThreads, grid);
-  return MOE_NORM_LAUNCH(norm_before_backward_kernel, g, wide, s, grid, smem, st);
+  const int mode = mode_of(wide, smem, {&g.ring.in[1], &g.ring.in[2], &g.dx}, {&g.ring.in[0]});
+  return MOE_NORM_LAUNCH(norm_before_backward_kernel, g, mode, s, grid, smem, st);
 }
 
 cudaError_t launch_norm_after_backward(NormAfterBackward g, bool wide, int num_sms, cudaStream_t st) {
   const Shape s = shape_of(g.H);
   const int64_t grid = norm_backward_rows(g.T, g.H, num_sms);
   const int smem = prepare(&g, s, wide, kBackwardThreads, grid);
-  return MOE_NORM_LAUNCH(norm_after_backward_kernel, g, wide, s, grid, smem, st);
+  const int mode = mode_of(wide, smem, {&g.ring.in[0]}, {&g.ring.in[1], &g.ring.in[2], &g.dy});
+  return MOE_NORM_LAUNCH(norm_after_backward_kernel, g, mode, s, grid, smem, st);
 }
 
 cudaError_t launch_column_sum(const ColumnSum& g, cudaStream_t st) {
