@@ -161,7 +161,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     for d in inc:
         cmd += ["-isystem" if d != INCLUDE else "-I", d]
-    cmd += [src, "-o", BINDING, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-L" + PKG,
+    cmd += [src, "-o", BINDING, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L" + PKG,
             "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -371,7 +371,7 @@ moe_status_t moe_linear_fp4(const moe_tensor_t* x, const moe_tensor_t* weight, i
   a.out = static_cast<__nv_bfloat16*>(out->data);
   a.os0 = out->strides[0];
   a.os1 = out->strides[1];
-  const bool rows = linear_fp4_by_rows(a.T, a.K);
+  const bool rows = linear_fp4_by_rows(a.T, a.N, a.K);
   const LinearFp4Plan p = linear_fp4_plan(a.T, a.N, a.K, nv);
   if (!rows) {
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;

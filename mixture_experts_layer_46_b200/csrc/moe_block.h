@@ -170,7 +170,7 @@ struct LinearFp4Plan {
   int64_t x_atoms, w_atoms;
   size_t codes_off, x_off, w_off, total;
 };
-bool linear_fp4_by_rows(int64_t T, int64_t K);
+bool linear_fp4_by_rows(int64_t T, int64_t N, int64_t K);
 LinearFp4Plan linear_fp4_plan(int64_t T, int64_t N, int64_t K, bool nv);
 cudaError_t launch_linear_fp4_rows(const LinearFp4& a, int num_sms, cudaStream_t st);
 // maps: x codes, weight codes, x scale atoms, weight scale atoms

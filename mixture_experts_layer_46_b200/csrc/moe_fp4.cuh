@@ -123,7 +123,9 @@ __device__ __forceinline__ uint32_t nv_quant16(const float* v, float amax, float
   if (sc == 0u) return 0u;
   const float s = e4m3x2_floats(sc).x;
   if (!far) {
-    const float inv = __frcp_rn(s * G), down = inv * kDown, up = inv * kUp;
+    float inv;  // (within one ulp: far inside the 2^-20 that the two roundings are apart)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s * G));
+    const float down = inv * kDown, up = inv * kUp;
     nv_codes16(v, s, G, down, up, w);
   } else {
 #pragma unroll

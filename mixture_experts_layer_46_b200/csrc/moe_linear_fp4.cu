@@ -2,7 +2,7 @@
 // factors e2m1 codes with a scale per block of K (e8m0 per 32, or e4m3 per 16 times one float),
 // x quantised on the way in.
 //
-// More than kRowsMaxT tokens (two launches):
+// More than a few tokens (two launches):
 //   1. fp4_prepare: x -> codes [T, K/2] and scales, and the weight's scales, both placed in the
 //      128-row x 4-scale atoms that the tensor core reads (byte (row % 32) * 16 + (row / 32) * 4
 //      + scale), one contiguous run a k-step of 256 elements and tile.  Bound by the read of x.
@@ -12,7 +12,7 @@
 //      accumulators (448 columns) and the scales (48) in the 512 columns of TMEM, so the
 //      epilogue of a tile runs under the next tile's products; a tile of 256 would read a
 //      tenth fewer bytes a product and stall for its epilogue.
-// Up to kRowsMaxT tokens (one launch): the weights' bytes are the work; every block quantises
+// One to four tokens (one launch): the weights' bytes are the work; every block quantises
 // the few rows of x into shared memory, a warp takes a weight row at a time.  The products of
 // two e2m1 numbers are multiples of 1/4 of at most 36, so eight of them add up exactly in a
 // half; each block of 16 is then scaled and added in fp32.
@@ -115,7 +115,7 @@ struct FpPrepare {
   int wide;
   int64_t T, K, N;
   int num_k, ntile, nh;   // k-steps, weight rows a tile, 128-row blocks a tile
-  int64_t row_tiles, x_blocks, n_nt;  // 32-row tiles and blocks of x, tiles of the weight
+  int64_t row_tiles, x_blocks, n_nt;  // 16-row tiles and blocks of x, tiles of the weight
   const float* x_global;
   uint8_t* codes;         // [T, num_k * 128]
   uint8_t* x_atoms;       // [128-row block][k-step][atom]
@@ -124,14 +124,13 @@ struct FpPrepare {
   uint8_t* w_atoms;       // [tile][k-step][atom][block]
 };
 
-// Blocks of 16 x 16 threads.  The first x_blocks walk over tiles of 32 rows x 256 elements of x,
-// a thread 16 neighbours of two rows, the next tile's on their way while the last ones are
-// quantised (blocks of one tile each spent their time starting up: 30 us instead of 16 at
-// T = 8192, K = 4096); the others place the weight's scales.  kFast: bf16, 16-byte loads.
+// Blocks of 16 x 16 threads.  The first x_blocks walk over tiles of 16 rows x 256 elements of x,
+// a thread 16 neighbours of a row, the next tile's on their way while the last ones are quantised;
+// the others place the weight's scales.  T = 8192, K = 4096: 23 us, the instructions of the two
+// roundings and the ties bound it (e8m0 scales 17 us; reading x and writing the codes 13 us).  kFast: bf16, 16-byte loads.
 template <bool kNv, bool kFast>
 __global__ void __launch_bounds__(256, 4) fp4_prepare_kernel(const FpPrepare g) {
   constexpr int kAtoms = atoms_per_step<kNv>();
-  constexpr int kRows = 2;
   pdl_wait();
   pdl_launch_dependents();
   if (blockIdx.x < g.x_blocks) {
@@ -145,68 +144,62 @@ __global__ void __launch_bounds__(256, 4) fp4_prepare_kernel(const FpPrepare g) 
     const int step = static_cast<int>(blockIdx.x % g.num_k), c = step * 256 + tx * 16;
     const int64_t first = blockIdx.x / g.num_k, stride = g.x_blocks / g.num_k;
     const bool cols = c < g.K;
-    uint4 next[kRows][2];
+    uint4 next[2];
     auto fetch = [&](int64_t rb) {
-#pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        const int64_t row = rb * (16 * kRows) + 16 * j + ty;
-        if (row < g.T && cols) {
-          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.x.data) + row * g.x.s0 + c);
-          next[j][0] = p[0];
-          next[j][1] = p[1];
-        }
+      const int64_t row = rb * 16 + ty;
+      if (row < g.T && cols) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.x.data) + row * g.x.s0 + c);
+        next[0] = p[0];
+        next[1] = p[1];
       }
     };
     if (kFast) fetch(first);
     for (int64_t rb = first; rb < g.row_tiles; rb += stride) {
-      uint4 cur[kRows][2];
-#pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        cur[j][0] = next[j][0];
-        cur[j][1] = next[j][1];
-      }
+      const uint4 cur[2] = {next[0], next[1]};
       if (kFast) fetch(rb + stride);
+      const int64_t row = rb * 16 + ty;
+      uint32_t sc = 0;
+      if (row < g.T && cols) {
+        float v[16], amax;
+        if constexpr (kFast) {
+          const uint32_t w[8] = {cur[0].x, cur[0].y, cur[0].z, cur[0].w,
+                                 cur[1].x, cur[1].y, cur[1].z, cur[1].w};
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        const int64_t row = rb * (16 * kRows) + 16 * j + ty;
-        uint32_t sc = 0;
-        if (row < g.T && cols) {
-          float v[16];
-          if constexpr (kFast) {
-            const uint32_t w[8] = {cur[j][0].x, cur[j][0].y, cur[j][0].z, cur[j][0].w,
-                                   cur[j][1].x, cur[j][1].y, cur[j][1].z, cur[j][1].w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              v[2 * i] = __uint_as_float(w[i] << 16);
-              v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-          } else {
-            read16(g.x, g.wide, row, c, v);
+          for (int i = 0; i < 8; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
           }
-          uint32_t w[2];
-          float amax = amax16(v);
-          if constexpr (kNv) {
-            sc = nv_quant16(v, amax, G, inv6, w);
-          } else {
-            // (K is a multiple of 32: both threads of a block are here)
-            amax = fmaxf(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30), amax, 1));
-            const int e = mx_scale_exp(amax);
-            const float f = exp2i_neg(e);
-            w[0] = cvt_e2m1x8(v, f);
-            w[1] = cvt_e2m1x8(v + 8, f);
-            sc = static_cast<uint32_t>(e + 127);
-          }
-          *reinterpret_cast<uint2*>(g.codes + row * (static_cast<int64_t>(g.num_k) * 128) + (c >> 1)) = make_uint2(w[0], w[1]);
-        }
-        // the threads of an atom's word (four blocks of 16, or of 32) hand their scales to the first
-        constexpr int kStep = kNv ? 1 : 2;  // threads a scale
+          // magnitudes order as integers: two a step
+          uint32_t m = 0;
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) sc |= __shfl_down_sync(0xffffffffu, sc, o * kStep) << (8 * o);
-        if (tx % (4 * kStep) == 0) {
-          const int r = static_cast<int>(row & 127);
-          *reinterpret_cast<uint32_t*>(g.x_atoms + (((row >> 7) * g.num_k + step) * kAtoms + tx / (4 * kStep)) * kAtomBytes +
-                                       (r & 31) * 16 + (r >> 5) * 4) = sc;
+          for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+          amax = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+        } else {
+          read16(g.x, g.wide, row, c, v);
+          amax = amax16(v);
         }
+        uint32_t w[2];
+        if constexpr (kNv) {
+          sc = nv_quant16(v, amax, G, inv6, w);
+        } else {
+          // (K is a multiple of 32: both threads of a block are here)
+          amax = fmaxf(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30), amax, 1));
+          const int e = mx_scale_exp(amax);
+          const float f = exp2i_neg(e);
+          w[0] = cvt_e2m1x8(v, f);
+          w[1] = cvt_e2m1x8(v + 8, f);
+          sc = static_cast<uint32_t>(e + 127);
+        }
+        *reinterpret_cast<uint2*>(g.codes + row * (static_cast<int64_t>(g.num_k) * 128) + (c >> 1)) = make_uint2(w[0], w[1]);
+      }
+      // the threads of an atom's word (four blocks of 16, or of 32) hand their scales to the first
+      constexpr int kStep = kNv ? 1 : 2;  // threads a scale
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) sc |= __shfl_down_sync(0xffffffffu, sc, o * kStep) << (8 * o);
+      if (tx % (4 * kStep) == 0) {
+        const int r = static_cast<int>(row & 127);
+        *reinterpret_cast<uint32_t*>(g.x_atoms + (((row >> 7) * g.num_k + step) * kAtoms + tx / (4 * kStep)) * kAtomBytes +
+                                     (r & 31) * 16 + (r >> 5) * 4) = sc;
       }
     }
     return;
@@ -542,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- a few rows
 
-constexpr int kRowsThreads = 512;
+constexpr int kRowsThreads = 256;
 
 struct FpRows {
   RowView x;
@@ -562,62 +555,72 @@ struct FpRows {
 // x in shared memory: halves [T][group of 32][4 parts of 16 bytes, turned by the group] and the
 // scales of each group of 16 (kNv) or 32 as floats.
 template <bool kNv, int kT>
-__global__ void __launch_bounds__(kRowsThreads) linear_fp4_rows_kernel(const FpRows g) {
+__global__ void __launch_bounds__(kRowsThreads, kT <= 2 ? 4 : 2) linear_fp4_rows_kernel(const FpRows g) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kScales = kNv ? 2 : 1;
   const int G = g.groups;
   uint8_t* xh = smem;
   float* xs = reinterpret_cast<float*>(smem + static_cast<size_t>(kT) * G * 64);
   const int lane = threadIdx.x & 31;
+  uint4 wv[4];
+  uint32_t sv[4];
+  // 128 blocks of 32 of a weight row: codes and scales, a lane four of them
+  auto fetch = [&](int64_t n, int c0) {
+    const uint8_t* wr = g.w + n * g.w_ld;
+    const uint8_t* sr = g.w_sf + n * g.ws0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + 32 * u;
+      wv[u] = make_uint4(0, 0, 0, 0);
+      sv[u] = 0;
+      if (c < G) {
+        wv[u] = *reinterpret_cast<const uint4*>(wr + c * 16);
+        sv[u] = sr[c * kScales * g.ws1];
+        if (kNv) sv[u] |= static_cast<uint32_t>(sr[(2 * c + 1) * g.ws1]) << 8;
+      }
+    }
+  };
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kRowsThreads / 32);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5);
   pdl_wait();
   pdl_launch_dependents();
+  if (first < g.N) fetch(first, lane);  // on their way while x is quantised
   const float xg = kNv ? *g.x_global : 1.0f;
-  for (int i = threadIdx.x; i < kT * G; i += kRowsThreads) {
-    const int t = i / G, c = i - t * G;
-    float v[32];
-    read32(g.x, g.wide, t, c * 32, v);
-    uint32_t w[4];
-    const uint32_t sc = quant32<kNv>(v, xg, w);
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      uint4 h;
-      h.x = e2m1x2_halves(w[p] & 0xffu);
-      h.y = e2m1x2_halves((w[p] >> 8) & 0xffu);
-      h.z = e2m1x2_halves((w[p] >> 16) & 0xffu);
-      h.w = e2m1x2_halves(w[p] >> 24);
-      *reinterpret_cast<uint4*>(xh + (static_cast<size_t>(i) * 4 + ((p ^ (c >> 1)) & 3)) * 16) = h;
-    }
-    if (kNv) {
-      const float2 s = e4m3x2_floats(sc);
-      xs[2 * i] = s.x;
-      xs[2 * i + 1] = s.y;
+  for (int i = threadIdx.x; i < kT * G * 2; i += kRowsThreads) {  // blocks of 16 (G is whole: pairs stay together)
+    const int t = i / (2 * G), c16 = i - t * 2 * G, c = c16 >> 1;
+    float v[16];
+    read16(g.x, g.wide, t, c16 * 16, v);
+    uint32_t w[2];
+    const float amax = amax16(v);
+    if constexpr (kNv) {
+      xs[i] = e4m3x2_floats(nv_quant16(v, amax, xg, 1.0f / (6.0f * xg), w)).x;
     } else {
-      xs[i] = exp2i_neg(127 - static_cast<int>(sc));
+      const float both = fmaxf(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30), amax, 1));
+      const int e = mx_scale_exp(both);
+      const float f = exp2i_neg(e);
+      w[0] = cvt_e2m1x8(v, f);
+      w[1] = cvt_e2m1x8(v + 8, f);
+      if ((c16 & 1) == 0) xs[t * G + c] = exp2i_neg(-e);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint4 h;
+      h.x = e2m1x2_halves(w[q] & 0xffu);
+      h.y = e2m1x2_halves((w[q] >> 8) & 0xffu);
+      h.z = e2m1x2_halves((w[q] >> 16) & 0xffu);
+      h.w = e2m1x2_halves(w[q] >> 24);
+      const int p = 2 * (c16 & 1) + q;
+      *reinterpret_cast<uint4*>(xh + (static_cast<size_t>(t * G + c) * 4 + ((p ^ (c >> 1)) & 3)) * 16) = h;
     }
   }
   __syncthreads();
   const float scale = xg * (g.w_global ? *g.w_global : 1.0f);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kRowsThreads / 32);
-  for (int64_t n = static_cast<int64_t>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5); n < g.N; n += stride) {
-    const uint8_t* wr = g.w + n * g.w_ld;
-    const uint8_t* sr = g.w_sf + n * g.ws0;
+  for (int64_t n = first; n < g.N; n += stride) {
     float acc[kT];
 #pragma unroll
     for (int t = 0; t < kT; ++t) acc[t] = 0.0f;
     for (int c0 = lane; c0 < G; c0 += 128) {
-      uint4 wv[4];
-      uint32_t sv[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = c0 + 32 * u;
-        wv[u] = make_uint4(0, 0, 0, 0);
-        sv[u] = 0;
-        if (c < G) {
-          wv[u] = *reinterpret_cast<const uint4*>(wr + c * 16);
-          sv[u] = sr[c * kScales * g.ws1];
-          if (kNv) sv[u] |= static_cast<uint32_t>(sr[(2 * c + 1) * g.ws1]) << 8;
-        }
-      }
+      if (n != first || c0 != lane) fetch(n, c0);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int c = c0 + 32 * u;
@@ -695,7 +698,7 @@ cudaError_t launch_rows(const FpRows& r, int num_sms, cudaStream_t st) {
   cudaError_t rc = raise_smem(linear_fp4_rows_kernel<kNv, kT>, kRowsSmemMax, configured);
   if (rc != cudaSuccess) return rc;
   int64_t blocks = (r.N + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
-  if (blocks > 2 * num_sms) blocks = 2 * num_sms;
+  if (blocks > 4 * num_sms) blocks = 4 * num_sms;
   return launch_pdl(linear_fp4_rows_kernel<kNv, kT>, dim3(static_cast<unsigned>(blocks)), dim3(kRowsThreads), smem, st, r);
 }
 
@@ -719,11 +722,15 @@ int tile_of(int64_t T, int64_t N) {
 
 }  // namespace
 
-bool linear_fp4_by_rows(int64_t T, int64_t K) { return T <= 4 && T * (K / 32) * 72 <= static_cast<int64_t>(kRowsSmemMax); }
+// Every token costs a read of x from shared memory for every weight: 4096 x 4096 takes 8.6, 11.5 and
+// 16.9 us for 1, 2 and 4 tokens, 12.6 on the pairs; a small matrix is over before two launches are.
+bool linear_fp4_by_rows(int64_t T, int64_t N, int64_t K) {
+  return T <= (N * K <= (1 << 22) ? 4 : 2) && T * (K / 32) * 72 <= static_cast<int64_t>(kRowsSmemMax);
+}
 
 LinearFp4Plan linear_fp4_plan(int64_t T, int64_t N, int64_t K, bool nv) {
   LinearFp4Plan p = {};
-  if (linear_fp4_by_rows(T, K)) return p;
+  if (linear_fp4_by_rows(T, N, K)) return p;
   const int64_t atoms = nv ? 4 : 2;
   p.num_k = (K + kStepElems - 1) / kStepElems;
   p.ntile = tile_of(T, N);
@@ -783,7 +790,7 @@ cudaError_t launch_pair_path(const LinearFp4& a, const LinearFp4Plan& p, const C
   f.ntile = p.ntile;
   f.nh = p.nh;
   f.n_nt = p.n_nt;
-  f.row_tiles = p.n_mt * 2 * kTokRows / 32;
+  f.row_tiles = p.n_mt * 2 * kTokRows / 16;
   int64_t per_step = 4 * num_sms / p.num_k;  // resident blocks
   per_step = per_step < 1 ? 1 : per_step > f.row_tiles ? f.row_tiles : per_step;
   f.x_blocks = per_step * p.num_k;

@@ -6,7 +6,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -96,7 +96,7 @@ struct Call {
     stream = reinterpret_cast<moe_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
   }
   at::Tensor empty(at::IntArrayRef sizes, at::ScalarType t) const {
-    return at::empty(sizes, at::TensorOptions().dtype(t).device(device));
+    return at::detail::empty_cuda(sizes, t, device, std::nullopt);  // (without the dispatcher: half the time)
   }
   at::Tensor given(const at::Tensor* t, at::IntArrayRef sizes, at::ScalarType type) const {
     return t ? *t : empty(sizes, type);
