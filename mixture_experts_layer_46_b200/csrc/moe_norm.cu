@@ -35,6 +35,51 @@ struct Vec8 {
   float v[8];
 };
 
+// Arithmetic on eight floats, two an instruction.
+__device__ __forceinline__ uint64_t pair(const Vec8& a, int i) {
+  return static_cast<uint64_t>(__float_as_uint(a.v[2 * i])) | (static_cast<uint64_t>(__float_as_uint(a.v[2 * i + 1])) << 32);
+}
+__device__ __forceinline__ uint64_t both(float f) {
+  return static_cast<uint64_t>(__float_as_uint(f)) | (static_cast<uint64_t>(__float_as_uint(f)) << 32);
+}
+__device__ __forceinline__ void set_pair(Vec8& a, int i, uint64_t p) {
+  a.v[2 * i] = __uint_as_float(static_cast<uint32_t>(p));
+  a.v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(p >> 32));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// a *= f
+__device__ __forceinline__ void scale8(Vec8& a, float f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) set_pair(a, i, mul2(pair(a, i), both(f)));
+}
+// a *= b
+__device__ __forceinline__ void mul8(Vec8& a, const Vec8& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) set_pair(a, i, mul2(pair(a, i), pair(b, i)));
+}
+// a += f b
+__device__ __forceinline__ void axpy8(Vec8& a, float f, const Vec8& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) set_pair(a, i, fma2(pair(b, i), both(f), pair(a, i)));
+}
+// acc (two floats) += a b
+__device__ __forceinline__ void dot8(uint64_t& acc, const Vec8& a, const Vec8& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc = fma2(pair(a, i), pair(b, i), acc);
+}
+__device__ __forceinline__ float sum_of(uint64_t acc) {
+  return __uint_as_float(static_cast<uint32_t>(acc)) + __uint_as_float(static_cast<uint32_t>(acc >> 32));
+}
+
 // How a kernel reads its row tensors: through the strides, 16 bytes a load, or from the ring.  The
 // ring comes in three forms: any types, all bf16, and a float stream around a bf16 block; known
 // types halve the instructions, which bound the ring otherwise (T=16384 H=4096 bf16, after + next:
@@ -344,18 +389,17 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(is_rin
     for (int v = 0; v < kVec; ++v) input8<kMode>(ring, 0, xt, t, v, g.H, raw[v]);
     if (is_ring(kMode)) ring.next(t, g.T);
     Vec8 x[kVec];
-    float ss = 0.0f;
+    uint64_t ss = 0;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       x[v] = unpack8<kMode>(raw[v], xt);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[v].v[i] * x[v].v[i];
+      dot8(ss, x[v], x[v]);
     }
-    const float r = inv_root(block_sum<kMaxThreads>(ss, scratch, turn), inv_h, g.eps);
+    const float r = inv_root(block_sum<kMaxThreads>(sum_of(ss), scratch, turn), inv_h, g.eps);
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[v].v[i] *= r * w[v].v[i];
+      scale8(x[v], r);
+      mul8(x[v], w[v]);
       store8<kMode>(g.out, block_type<kMode>(g.out), t, v, g.H, x[v]);
     }
     if (g.rstd && threadIdx.x == 0) g.rstd[t * g.rstd_s] = r;
@@ -416,46 +460,41 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(is_rin
     for (int v = 0; v < kVec; ++v) o[v] = unpack8<kMode>(y[v], yt);
     float r = 1.0f;
     if (g.normalize) {
-      float ss = 0.0f;
+      uint64_t ss = 0;
 #pragma unroll
-      for (int v = 0; v < kVec; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss += o[v].v[i] * o[v].v[i];
-      r = inv_root(block_sum<kMaxThreads>(ss, scratch, turn), inv_h, g.eps);
+      for (int v = 0; v < kVec; ++v) dot8(ss, o[v], o[v]);
+      r = inv_root(block_sum<kMaxThreads>(sum_of(ss), scratch, turn), inv_h, g.eps);
     }
     if (g.rstd && threadIdx.x == 0) g.rstd[t * g.rstd_s] = r;
     f *= r;
-    float ss = 0.0f;
+    uint64_t ss = 0;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[v].v[i] *= f * w[v].v[i];
+      scale8(o[v], f);
+      mul8(o[v], w[v]);
       if (gate_full) {
         if (is_ring(kMode)) input8<kMode>(ring, 2, gtt, t, v, g.H, gt[v]);
         Vec8 c = unpack8<kMode>(gt[v], gtt);
         gate_values(c, g.act);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[v].v[i] *= c.v[i];
+        mul8(o[v], c);
       }
       if (have_x) {
         if (is_ring(kMode)) input8<kMode>(ring, 1, xt, t, v, g.H, x[v]);
         const Vec8 c = unpack8<kMode>(x[v], xt);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[v].v[i] += g.alpha * c.v[i];
+        axpy8(o[v], g.alpha, c);
       }
       store8<kMode>(g.out, stream_type<kMode>(g.out), t, v, g.H, o[v]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += o[v].v[i] * o[v].v[i];
+      dot8(ss, o[v], o[v]);
     }
     if (is_ring(kMode)) ring.next(t, g.T);
     if (want_next) {
-      const float rn = inv_root(block_sum<kMaxThreads>(ss, scratch, turn), inv_h, g.eps);
+      const float rn = inv_root(block_sum<kMaxThreads>(sum_of(ss), scratch, turn), inv_h, g.eps);
       if (g.next_rstd && threadIdx.x == 0) g.next_rstd[t * g.next_rstd_s] = rn;
       if (g.nxt.data) {
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[v].v[i] *= rn * wn[v].v[i];
+          scale8(o[v], rn);
+          mul8(o[v], wn[v]);
           store8<kMode>(g.nxt, block_type<kMode>(g.nxt), t, v, g.H, o[v]);
         }
       }
@@ -510,29 +549,26 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
       if (!is_ring(kMode) && have_res) input8<kMode>(ring, 2, rt, t, v, g.H, res[v]);
     }
     Vec8 p[kVec], x[kVec];
-    float dot = 0.0f;
+    uint64_t dot = 0;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       p[v] = unpack8<kMode>(rd[v], dt);
       x[v] = unpack8<kMode>(rx[v], xt);
+      scale8(x[v], r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[v].v[i] *= r;
-        dw[v].v[i] += p[v].v[i] * x[v].v[i];
-        p[v].v[i] *= w[v].v[i];
-        dot += p[v].v[i] * x[v].v[i];
-      }
+      for (int i = 0; i < 4; ++i) set_pair(dw[v], i, fma2(pair(p[v], i), pair(x[v], i), pair(dw[v], i)));
+      mul8(p[v], w[v]);
+      dot8(dot, p[v], x[v]);
     }
-    const float c = block_sum<kMaxThreads>(dot, scratch, turn) * inv_h;
+    const float c = block_sum<kMaxThreads>(sum_of(dot), scratch, turn) * inv_h;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[v].v[i] = r * (p[v].v[i] - x[v].v[i] * c);
+      axpy8(p[v], -c, x[v]);
+      scale8(p[v], r);
       if (have_res) {
         if (is_ring(kMode)) input8<kMode>(ring, 2, rt, t, v, g.H, res[v]);
         const Vec8 d = unpack8<kMode>(res[v], rt);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[v].v[i] += g.alpha * d.v[i];
+        axpy8(p[v], g.alpha, d);
       }
       store8<kMode>(g.dx, stream_type<kMode>(g.dx), t, v, g.H, p[v]);
     }
@@ -595,43 +631,44 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
       if (!is_ring(kMode) && gate_full) input8<kMode>(ring, 2, gtt, t, v, g.H, rg[v]);
     }
     Vec8 d[kVec], y[kVec];
-    float dot = 0.0f, gsum = 0.0f;
+    uint64_t dot = 0, gsum = 0;
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       d[v] = unpack8<kMode>(rd[v], dt);
       y[v] = unpack8<kMode>(ry[v], yt);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[v].v[i] *= r;
+      scale8(y[v], r);
       if (gate_full) {
         if (is_ring(kMode)) input8<kMode>(ring, 2, gtt, t, v, g.H, rg[v]);
         Vec8 c = unpack8<kMode>(rg[v], gtt);
         if (g.dgate.data) {
           Vec8 e = c;
           gate_slopes(e, g.act);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e.v[i] *= d[v].v[i] * y[v].v[i] * w[v].v[i];
+          mul8(e, d[v]);
+          mul8(e, y[v]);
+          mul8(e, w[v]);
           store8<kMode>(g.dgate, g.dgate.dtype, t, v, g.H, e);
         }
         gate_values(c, g.act);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[v].v[i] *= c.v[i];
+        mul8(d[v], c);
       }
       // the column sum of dout yh: times a(g) it is dw, and for a gate that is the same in every
       // row of the column times w a'(g) it is dg, so one sum serves both there
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = d[v].v[i] * y[v].v[i];
-        dw[v].v[i] += rowv * e;
-        if (gate_row) gsum += e * w[v].v[i];
-        d[v].v[i] *= rowv * w[v].v[i];
-        dot += d[v].v[i] * y[v].v[i];
+      if (gate_row) {
+        Vec8 e = d[v];
+        mul8(e, y[v]);
+        dot8(gsum, e, w[v]);
+        scale8(d[v], rowv);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) set_pair(dw[v], i, fma2(pair(d[v], i), pair(y[v], i), pair(dw[v], i)));
+      mul8(d[v], w[v]);
+      dot8(dot, d[v], y[v]);
     }
     if (is_ring(kMode)) ring.next(t, g.T);
     float c = 0.0f;
-    if (g.normalize) c = block_sum<kMaxThreads>(dot, scratch, turn) * inv_h;
+    if (g.normalize) c = block_sum<kMaxThreads>(sum_of(dot), scratch, turn) * inv_h;
     if (gate_row && g.dgate.data) {
-      const float s = block_sum<kMaxThreads>(gsum, scratch, turn);
+      const float s = block_sum<kMaxThreads>(sum_of(gsum), scratch, turn);
       if (g.gate_mode == kGateOne) {
         dall += s;
       } else if (threadIdx.x == 0) {
@@ -645,9 +682,9 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
     }
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[v].v[i] = r * (d[v].v[i] - y[v].v[i] * c);
-      store8<kMode>(g.dy, block_type<kMode>(g.dy), t, v, g.H, y[v]);
+      axpy8(d[v], -c, y[v]);
+      scale8(d[v], r);
+      store8<kMode>(g.dy, block_type<kMode>(g.dy), t, v, g.H, d[v]);
     }
   }
   if (g.part) store_partial<kVec, kMode>(g.part, g.H, dw);
