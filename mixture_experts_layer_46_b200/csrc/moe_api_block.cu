@@ -95,9 +95,13 @@ bool norm_shape_ok(const moe_tensor_t* t, float eps) {
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// the partial column sums of a norm's gradient
+// rows of partial column sums of a norm's gradient, either way its rows are read
+size_t norm_partial_rows(int64_t T, int64_t H) {
+  const int64_t a = norm_backward_rows(T, H, true, kNormMaxSms), b = norm_backward_rows(T, H, false, kNormMaxSms);
+  return static_cast<size_t>(a > b ? a : b);
+}
 size_t norm_partial_bytes(int64_t T, int64_t H) {
-  const size_t rows = static_cast<size_t>(norm_backward_rows(T, H, kNormMaxSms));
+  const size_t rows = norm_partial_rows(T, H);
   return round256((rows > 0 ? rows : 1) * static_cast<size_t>(H) * sizeof(float));
 }
 
@@ -182,7 +186,7 @@ moe_status_t moe_norm_after(const moe_tensor_t* y, const moe_tensor_t* residual,
 
 size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t H) {
   if (T < 0 || H < 1 || H > kNormMaxH) return 0;
-  const size_t rows = static_cast<size_t>(norm_backward_rows(T, H, kNormMaxSms));
+  const size_t rows = norm_partial_rows(T, H);
   return norm_partial_bytes(T, H) + round256((rows > 0 ? rows : 1) * sizeof(float));
 }
 
@@ -217,15 +221,15 @@ moe_status_t moe_norm_before_backward(const moe_tensor_t* dout, const moe_tensor
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   g.part = dweight ? static_cast<float*>(workspace) : nullptr;
   int launches = 0;
+  const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.ring.in[1]) &&
+                    wide_ok(g.ring.in[2]) && wide_ok(g.dx) && wide_ok(g.w);
   if (g.T > 0) {
-    const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.ring.in[1]) &&
-                      wide_ok(g.ring.in[2]) && wide_ok(g.dx) && wide_ok(g.w);
     const cudaError_t rc = launch_norm_before_backward(g, wide, sms, st);
     if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_before_backward");
     ++launches;
   }
   if (dweight) {
-    c.rows = static_cast<int>(norm_backward_rows(g.T, g.H, sms));
+    c.rows = static_cast<int>(norm_backward_rows(g.T, g.H, wide, sms));
     c.H = g.H;
     c.part = g.part;
     const cudaError_t rc = launch_column_sum(c, st);
@@ -280,16 +284,16 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
                     ? reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes)
                     : nullptr;
   int launches = 0;
+  const bool gate_rows = g.gate_mode == kGateFull || g.gate_mode == kGateChannel;
+  const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.ring.in[1]) && wide_ok(g.dy) && wide_ok(g.w) &&
+                    (!gate_rows || wide_ok(g.gate)) && (g.gate_mode != kGateFull || wide_ok(g.dgate));
   if (g.T > 0) {
-    const bool gate_rows = g.gate_mode == kGateFull || g.gate_mode == kGateChannel;
-    const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.ring.in[1]) && wide_ok(g.dy) && wide_ok(g.w) &&
-                      (!gate_rows || wide_ok(g.gate)) && (g.gate_mode != kGateFull || wide_ok(g.dgate));
     const cudaError_t rc = launch_norm_after_backward(g, wide, sms, st);
     if (rc != cudaSuccess) return api_cuda_fail(rc, "norm_after_backward");
     ++launches;
   }
   if (dweight || gate_sum) {
-    c.rows = static_cast<int>(norm_backward_rows(g.T, g.H, sms));
+    c.rows = static_cast<int>(norm_backward_rows(g.T, g.H, wide, sms));
     c.H = g.H;
     c.act = gate_act;
     c.gate_mode = g.gate_mode;

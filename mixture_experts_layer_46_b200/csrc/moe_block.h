@@ -105,7 +105,7 @@ struct ColumnSum {
 };
 
 // Blocks (= rows of partial column sums) of the gradient kernels.
-int64_t norm_backward_rows(int64_t T, int64_t H, int num_sms);
+int64_t norm_backward_rows(int64_t T, int64_t H, bool wide, int num_sms);
 // wide: every row tensor allows 16-byte accesses (see moe_norm.cu)
 cudaError_t launch_norm_before(NormBefore g, bool wide, int num_sms, cudaStream_t st);
 cudaError_t launch_norm_after(NormAfter g, bool wide, int num_sms, cudaStream_t st);

@@ -357,18 +357,20 @@ __device__ __forceinline__ float inv_root(float sum, float inv_h, float eps) {
   return a > 1e-30f && a < 1e30f ? r : y;
 }
 
-// Threads of resident blocks on an SM: 80 and 128 registers a thread, what the kernels need
-// without spilling up to 4096 elements a row (the ring, not the number of warps, keeps memory busy).
-constexpr int kRingThreads = 768, kDirectThreads = 512, kBackwardThreads = 512;
+// Threads of resident blocks on an SM, and rows on their way in a block's ring.  More of either
+// asks DRAM for too many streams at once: before + after + next at T=16384 H=4096 took 156 us with
+// 768 threads and four rows, 134 with 512 and four, 132 with 512 and three, 146 with two, 210
+// with 256.
+constexpr int kResident = 512;
+constexpr int64_t kRingBytes = 96 << 10;  // of an SM's blocks together
 constexpr int min_blocks(int threads_per_sm, int max_threads) {
   return threads_per_sm / max_threads < 1 ? 1 : threads_per_sm / max_threads;
 }
-constexpr int forward_threads(bool ring) { return ring ? kRingThreads : kDirectThreads; }
 
 // ---------------------------------------------------------------- forward
 
 template <int kVec, int kMode, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(is_ring(kMode)), kMaxThreads))
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(kResident, kMaxThreads))
     norm_before_kernel(const NormBefore g) {
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) float scratch[2][32];
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(is_rin
 // kept in registers unrounded between the two reductions, the weights (a per-channel gate
 // multiplied in) for all of the block's rows.
 template <int kVec, int kMode, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, min_blocks(forward_threads(is_ring(kMode)), kMaxThreads))
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(kResident, kMaxThreads))
     norm_after_kernel(const NormAfter g) {
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) float scratch[2][32];
@@ -517,7 +519,7 @@ __device__ __forceinline__ void store_partial(float* part, int H, const Vec8 (&a
 }
 
 template <int kVec, int kMode, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMaxThreads))
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(kResident, kMaxThreads))
     norm_before_backward_kernel(const NormBeforeBackward g) {
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) float scratch[2][32];
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMax
 }
 
 template <int kVec, int kMode, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, min_blocks(kBackwardThreads, kMaxThreads))
+__global__ void __launch_bounds__(kMaxThreads, min_blocks(kResident, kMaxThreads))
     norm_after_backward_kernel(const NormAfterBackward g) {
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) float scratch[2][32];
@@ -747,9 +749,11 @@ __global__ void __launch_bounds__(32 * kStrips) column_sum_kernel(const ColumnSu
 struct Shape {
   int vec, threads;
 };
-Shape shape_of(int64_t H) {
+Shape shape_of(int64_t H, bool wide) {
   const int n = static_cast<int>((H + 7) / 8);
-  const int vec = n <= 256 ? 1 : 2;
+  // (two slots halve what a row costs besides its elements: T=16384 H=1024 after + next 41 -> 33 us;
+  // through the strides, where an element is a load, one is faster: 1023 x 1407 f32 16 against 20)
+  const int vec = n <= (wide ? 64 : 256) ? 1 : 2;
   Shape s;
   s.vec = vec;
   s.threads = ((n + vec - 1) / vec + 31) / 32 * 32;
@@ -764,8 +768,8 @@ int64_t blocks_of(int64_t T, int threads, int num_sms, int threads_per_sm) {
   return T < g ? T : g;
 }
 
-// The ring of a wide call in which blocks walk over several rows: as many stages (up to 4) as
-// let `per_sm` blocks share an SM's 220 KB; none where the rows do not fit.
+// The ring of a wide call in which blocks walk over several rows: as many stages (two to eight) as
+// fit kRingBytes on an SM of `per_sm` blocks; none where two rows do not fit its 220 KB.
 int ring_of(RowRing* r, int H, int64_t T, int64_t grid, int per_sm) {
   r->stage_bytes = 0;
   for (int i = 0; i < 3; ++i) {
@@ -776,7 +780,9 @@ int ring_of(RowRing* r, int H, int64_t T, int64_t grid, int per_sm) {
   }
   const int64_t room = (220 << 10) / per_sm - 1024 - 128;
   int64_t n = room / r->stage_bytes;
-  if (n > 4) n = 4;
+  const int64_t want = kRingBytes / (per_sm * r->stage_bytes);
+  if (n > want) n = want < 2 ? 2 : want;
+  if (n > 8) n = 8;
   const int64_t rows = (T + grid - 1) / grid;
   if (n > rows) n = rows;
   r->stages = static_cast<int>(n);
@@ -833,38 +839,38 @@ int prepare(Args* g, const Shape& s, bool wide, int threads_per_sm, int64_t grid
 
 }  // namespace
 
-int64_t norm_backward_rows(int64_t T, int64_t H, int num_sms) {
-  return blocks_of(T, shape_of(H).threads, num_sms < kNormMaxSms ? num_sms : kNormMaxSms, kBackwardThreads);
+int64_t norm_backward_rows(int64_t T, int64_t H, bool wide, int num_sms) {
+  return blocks_of(T, shape_of(H, wide).threads, num_sms < kNormMaxSms ? num_sms : kNormMaxSms, kResident);
 }
 
 cudaError_t launch_norm_before(NormBefore g, bool wide, int num_sms, cudaStream_t st) {
-  const Shape s = shape_of(g.H);
-  const int64_t grid = blocks_of(g.T, s.threads, num_sms, forward_threads(wide));
-  const int smem = prepare(&g, s, wide, forward_threads(wide), grid);
+  const Shape s = shape_of(g.H, wide);
+  const int64_t grid = blocks_of(g.T, s.threads, num_sms, kResident);
+  const int smem = prepare(&g, s, wide, kResident, grid);
   const int mode = mode_of(wide, smem, {&g.ring.in[0]}, {&g.out});
   return MOE_NORM_LAUNCH(norm_before_kernel, g, mode, s, grid, smem, st);
 }
 
 cudaError_t launch_norm_after(NormAfter g, bool wide, int num_sms, cudaStream_t st) {
-  const Shape s = shape_of(g.H);
-  const int64_t grid = blocks_of(g.T, s.threads, num_sms, forward_threads(wide));
-  const int smem = prepare(&g, s, wide, forward_threads(wide), grid);
+  const Shape s = shape_of(g.H, wide);
+  const int64_t grid = blocks_of(g.T, s.threads, num_sms, kResident);
+  const int smem = prepare(&g, s, wide, kResident, grid);
   const int mode = mode_of(wide, smem, {&g.ring.in[1], &g.out}, {&g.ring.in[0], &g.ring.in[2], &g.nxt});
   return MOE_NORM_LAUNCH(norm_after_kernel, g, mode, s, grid, smem, st);
 }
 
 cudaError_t launch_norm_before_backward(NormBeforeBackward g, bool wide, int num_sms, cudaStream_t st) {
-  const Shape s = shape_of(g.H);
-  const int64_t grid = norm_backward_rows(g.T, g.H, num_sms);
-  const int smem = prepare(&g, s, wide, kBackwardThreads, grid);
+  const Shape s = shape_of(g.H, wide);
+  const int64_t grid = norm_backward_rows(g.T, g.H, wide, num_sms);
+  const int smem = prepare(&g, s, wide, kResident, grid);
   const int mode = mode_of(wide, smem, {&g.ring.in[1], &g.ring.in[2], &g.dx}, {&g.ring.in[0]});
   return MOE_NORM_LAUNCH(norm_before_backward_kernel, g, mode, s, grid, smem, st);
 }
 
 cudaError_t launch_norm_after_backward(NormAfterBackward g, bool wide, int num_sms, cudaStream_t st) {
-  const Shape s = shape_of(g.H);
-  const int64_t grid = norm_backward_rows(g.T, g.H, num_sms);
-  const int smem = prepare(&g, s, wide, kBackwardThreads, grid);
+  const Shape s = shape_of(g.H, wide);
+  const int64_t grid = norm_backward_rows(g.T, g.H, wide, num_sms);
+  const int smem = prepare(&g, s, wide, kResident, grid);
   const int mode = mode_of(wide, smem, {&g.ring.in[0]}, {&g.ring.in[1], &g.ring.in[2], &g.dy});
   return MOE_NORM_LAUNCH(norm_after_backward_kernel, g, mode, s, grid, smem, st);
 }
