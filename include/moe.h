@@ -518,7 +518,9 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
  * Kernels: the way in (norm, router, choice); the experts, with bf16 weights and few tokens two
  * kernels over their rows with xn and h in fp32, else the kernels of moe_forward; the gate and the
  * residual are part of the last one, with post_norm = 1 or MXFP4 weights a kernel of their own.
- * NaN logits rank below every number.  Asynchronous on `stream`, no allocation.  T = 0 is a no-op. */
+ * NaN logits rank below every number.  Calls that take moe_forward's one-kernel decode (at most 32
+ * slots, MXFP4 weights or more tokens than the kernels over rows take) must not overlap on the GPU,
+ * as moe_forward_host_ws says; others may, with a workspace each.  Asynchronous on `stream`, no allocation.  T = 0 is a no-op. */
 enum { MOE_LAYER_MAX_TOKENS = 32 };
 
 size_t moe_layer_decode_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int32_t wdtype);
@@ -553,7 +555,7 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
  *   x_global,      [1] or 0-d f32 on the device: the float scales of the e4m3 form (there x_global is
  *   weight_global  required, weight_global NULL = 1); NULL with e8m0 scales
  *   out            [T, N] bf16, any strides, rounded once from the fp32 sum
- * K % 32 == 0.  One or two tokens (up to four where N K <= 2^22) run as one launch, more as two
+ * K % 32 == 0; T, N <= 2^24, K <= 2^20, T K and N K < 2^40.  One or two tokens (up to four where N K <= 2^22) run as one launch, more as two
  * (quantisation and placing of the scales; the product on the tensor cores).  Sums are fp32 in a
  * fixed order.  `workspace`: moe_linear_fp4_workspace_bytes, 256-byte aligned (not touched by
  * the one-launch form, which asks for 256 bytes); it must not be shared by calls that run at the same time.  T = 0 is a

@@ -117,6 +117,7 @@ moe_status_t scalar_of(const moe_tensor_t* t, const float** p) {
 constexpr int64_t kFp4MaxRows = int64_t(1) << 24, kFp4MaxK = int64_t(1) << 20;
 bool fp4_shape_ok(int64_t T, int64_t N, int64_t K, int32_t fmt) {
   return T >= 0 && T <= kFp4MaxRows && N >= 1 && N <= kFp4MaxRows && K >= 32 && K <= kFp4MaxK && K % 32 == 0 &&
+         T * K < (int64_t(1) << 40) && N * K < (int64_t(1) << 40) &&
          (fmt == MOE_SCALE_E8M0_32 || fmt == MOE_SCALE_E4M3_16);
 }
 

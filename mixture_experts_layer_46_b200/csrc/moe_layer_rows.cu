@@ -39,8 +39,9 @@ __device__ __forceinline__ void find_experts(const View2& ids, int T, int k, int
   int64_t id = -1;
   if (lane < S) {
     const int64_t off = (lane / k) * ids.s0 + (lane % k) * ids.s1;
-    id = ids.dtype == MOE_I64 ? static_cast<const int64_t*>(ids.data)[off]
-                              : static_cast<int64_t>(static_cast<const int32_t*>(ids.data)[off]);
+    // (from L2: the second kernel reads them before its wait)
+    id = ids.dtype == MOE_I64 ? __ldcg(static_cast<const long long*>(ids.data) + off)
+                              : static_cast<int64_t>(__ldcg(static_cast<const int*>(ids.data) + off));
   }
   const bool valid = id >= 0 && id < E;
   const int key = valid ? static_cast<int>(id) : -1 - lane;

@@ -224,3 +224,55 @@ def test_decode_steps_through_two_layers():
         check(la, layer64(dict(a, x=x), 2, pre=a["pre"]))
         check(lb, layer64(dict(b, x=la[0]), 2, pre=b["pre"], post=b["post"]))
         x = lb[0]
+
+
+@pytest.mark.parametrize("T,post", [(1, False), (3, True), (6, False)])
+def test_steps_in_flight(T, post):
+    """Many steps of changing routing in flight, the second kernel's early reads among them: the
+    bits of the same steps taken one at a time."""
+    H, I, E, k = 256, 512, 32, 2
+    s = make(31, T, H, I, E)
+    w13 = moe.w13_from_packed(s["w13"])
+    ws = torch.empty(moe.layer_decode_workspace_bytes(T, H, I, E, k), dtype=torch.uint8, device="cuda")
+    ids, wts = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    xs = [make(100 + i, T, H, 32, 1)["x"] for i in range(40)]
+    call = lambda x, out: moe.layer_decode(x, s["router"], w13, s["w2"], k, pre_weight=s["pre"], post_norm=post, out=out,
+                                           topk_ids=ids, topk_weights=wts, workspace=ws)
+    one = []
+    for x in xs:
+        one.append((call(x, None)[0], ids.clone()))
+        torch.cuda.synchronize()
+    outs = [torch.empty(T, H, dtype=BF, device="cuda") for _ in xs]
+    for x, o in zip(xs, outs):
+        call(x, o)
+    torch.cuda.synchronize()
+    assert len({tuple(i.flatten().tolist()) for _, i in one}) > 10
+    for (o, _), got in zip(one, outs):
+        assert torch.equal(o, got)
+
+
+def test_two_streams():
+    """Two calls at once, a workspace each."""
+    T, H, I, E, k = 2, 1024, 512, 16, 4
+    s = make(41, T, H, I, E)
+    w13 = moe.w13_from_packed(s["w13"])
+    xs = [make(200 + i, T, H, 32, 1)["x"] for i in range(20)]
+    want = [moe.layer_decode(x, s["router"], w13, s["w2"], k) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [moe.layer_decode(x, s["router"], w13, s["w2"], k, stream=streams[i % 2]) for i, x in enumerate(xs)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+
+
+def test_an_infinite_router_row_ranks_last():
+    s = make(51, 2, 256, 64, 8)
+    s["router"][3, 7] = float("inf")
+    out, ids, p = moe.layer_decode(s["x"], s["router"], moe.w13_from_packed(s["w13"]), s["w2"], 7)
+    xd = s["x"].double()
+    logits = (xd / (xd.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()) @ s["router"].double().T
+    logits[:, 3] = -float("inf")  # inf * x carries its rounding along as NaN, which ranks below every number
+    want = torch.sort(logits, dim=-1, descending=True, stable=True)[1][:, :7]
+    assert torch.equal(ids.long(), want)

@@ -122,7 +122,8 @@ def test_quantize_zero_scale_gives_zeros():
 
 SHAPES = [(1, 1, 32), (1, 64, 128), (1, 4096, 4096), (2, 77, 640), (3, 1000, 4096), (4, 33, 2976),      # by rows
           (5, 64, 128), (5, 1, 32), (31, 333, 96), (128, 224, 256), (129, 450, 288), (256, 2048, 512),  # on pairs
-          (257, 97, 1184), (1023, 1024, 4096), (700, 8192, 1024), (2500, 1111, 384), (16, 1024, 4096)]
+          (257, 97, 1184), (1023, 1024, 4096), (700, 8192, 1024), (2500, 1111, 384), (16, 1024, 4096),
+          (2049, 8000, 2048), (300, 8111, 1536), (515, 8190, 2080)]
 
 
 @pytest.mark.parametrize("form", ["nv", "mx"])
@@ -197,3 +198,41 @@ def test_linear_graph_and_stream():
         x.copy_(rows(T, T, 256))
         graph.replay()
         assert torch.equal(out, on_stream)
+
+
+def test_linear_two_streams():
+    """Calls at once on two streams, a workspace each (made by the call on its stream)."""
+    codes, sf, wg, _ = weight(1, 512, 512, "nv")
+    xs = [rows(i, 3 + 40 * (i % 3), 512) for i in range(12)]
+    xg = torch.tensor([0.01], device="cuda")
+    want = [moe.linear_fp4(x, codes, sf, x_global=xg, w_global=wg) for x in xs]
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [moe.linear_fp4(x, codes, sf, x_global=xg, w_global=wg, stream=st[i % 2]) for i, x in enumerate(xs)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_linear_far_offsets():
+    """An output of more than 2^31 elements: its last rows are the ones a small call gives."""
+    T, N, K = 1 << 19, 4104, 64
+    codes, sf, wg, _ = weight(5, N, K, "nv")
+    tail = rows(6, 300, K)
+    x = torch.zeros(T, K, dtype=BF, device="cuda")
+    x[-300:] = tail
+    xg = (tail.float().abs().max() / 2688.0).reshape(1)
+    out = moe.linear_fp4(x, codes, sf, x_global=xg, w_global=wg)
+    assert out.numel() > 1 << 31
+    assert torch.equal(out[-300:], moe.linear_fp4(tail, codes, sf, x_global=xg, w_global=wg))
+    assert int(out[: T - 300].count_nonzero()) == 0
+
+
+def test_quantise_then_multiply():
+    """The activations' quantiser and the linear layer agree: a layer of the quantised values alone."""
+    x, w = rows(1, 130, 256), rows(2, 200, 256, F32)
+    xc, xs, xg = moe.quantize_nvfp4(x)
+    wc, ws, wg = moe.quantize_nvfp4(w)
+    code = unpack(xc)
+    v = GRID.cuda()[code & 7] * torch.where(code >= 8, -1.0, 1.0) * (xs.double().repeat_interleave(16, 1) * xg.double())
+    check(moe.linear_fp4(x, wc, ws, x_global=xg, w_global=wg), v, nv64(w, wg)[2])

@@ -278,3 +278,34 @@ def test_streams_graphs_and_workspaces():
     assert torch.equal(o2, out)
     for a, b in zip((dy, dw, dg), want):
         assert torch.equal(a, b)
+
+
+def test_far_offsets():
+    """Rows past 2^31 elements: the last ones are those that a small call gives, both ways."""
+    T, H = 600_000, 4096
+    g = torch.Generator().manual_seed(3)
+    tail, w = rnd(g, 64, H), rnd(g, H)
+    x = torch.zeros(T, H, dtype=BF, device="cuda")
+    x[-64:] = tail
+    out, r = moe.norm_before(x, w)
+    want, rw = moe.norm_before(tail, w)
+    assert torch.equal(out[-64:], want) and torch.equal(r[-64:], rw)
+    dx, dw = moe.norm_before_backward(x, x, r, w, dx=out)
+    wdx, wdw = moe.norm_before_backward(tail, tail, rw, w)
+    assert torch.equal(dx[-64:], wdx)
+    assert bool(((dw - wdw).abs() <= 2.0 ** -12 * wdw.abs().max()).all())
+
+
+def test_two_streams_share_nothing():
+    """Gradients at once on two streams, workspaces of their own."""
+    g = torch.Generator().manual_seed(4)
+    xs = [rnd(g, 64 + i, 512) for i in range(10)]
+    w = rnd(g, 512)
+    r = [moe.norm_before(x, w)[1] for x in xs]
+    want = [moe.norm_before_backward(x, x, q, w) for x, q in zip(xs, r)]
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [moe.norm_before_backward(x, x, q, w, stream=st[i % 2]) for i, (x, q) in enumerate(zip(xs, r))]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
