@@ -309,3 +309,57 @@ def test_two_streams_share_nothing():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("T,H", [(1, 4096), (900, 4096), (2000, 1024), (70, 1407)])
+def test_in_place(T, H):
+    """An output on top of an input of its shape, or one tensor given twice: the bits of separate ones."""
+    g = torch.Generator().manual_seed(T + H)
+    y, x, w = rnd(g, T, H), rnd(g, T, H), rnd(g, H)
+    gate = rnd(g, T, H)
+    clone = lambda *ts: [t.clone() for t in ts]
+    want = moe.norm_before(x, w)
+    a, = clone(x)
+    assert torch.equal(moe.norm_before(a, w, out=a)[0], want[0]) and torch.equal(a, want[0])
+    want = moe.norm_after(y, x, w, gate, gate_act="tanh", next_weight=w)
+    for into in ("y", "x"):
+        a, b = clone(y, x)
+        got = moe.norm_after(a, b, w, gate, gate_act="tanh", next_weight=w, out=a if into == "y" else b)
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
+    twice = moe.norm_after(x, x, w)
+    assert torch.equal(twice[0], moe.norm_after(x.clone(), x, w)[0])
+    r, d = want[1], rnd(g, T, H)
+    want = moe.norm_before_backward(d, x, r, w, residual_grad=y, residual_scale=0.5)
+    for into in range(3):
+        ins = clone(d, x, y)
+        got = moe.norm_before_backward(ins[0], ins[1], r, w, residual_grad=ins[2], residual_scale=0.5, dx=ins[into])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    want = moe.norm_after_backward(d, y, r, w, gate)
+    for into in range(2):
+        ins = clone(d, y)
+        got = moe.norm_after_backward(ins[0], ins[1], r, w, gate, dy=ins[into])
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
+
+
+def test_a_block_as_it_trains():
+    """The norms around a block, run together: the gradient of a loss through norm, a linear block,
+    gate, scaled residual and the next norm, against differentiation in 64 bits."""
+    T, H, alpha = 40, 96, 0.7
+    g = torch.Generator().manual_seed(8)
+    x, wb, w0, w1, w2, gate, c = (rnd(g, T, H, dt=F32), rnd(g, H, H, dt=F32, scale=H ** -0.5), rnd(g, H, dt=F32),
+                                  rnd(g, H, dt=F32), rnd(g, H, dt=F32), rnd(g, 1, H, dt=F32), rnd(g, T, H, dt=F32))
+    xn, rx = moe.norm_before(x, w0)
+    y = xn @ wb
+    out, ry, nxt, rn = moe.norm_after(y, x, w1, gate, gate_act="sigmoid", residual_scale=alpha, next_weight=w2)
+    dout, dw2 = moe.norm_before_backward(c, out, rn, w2)
+    dy, dw1, dgate = moe.norm_after_backward(dout, y, ry, w1, gate, gate_act="sigmoid")
+    dx, dw0 = moe.norm_before_backward(dy @ wb.T, x, rx, w0, residual_grad=dout, residual_scale=alpha)
+    L = [t.to(D).requires_grad_() for t in (x, w0, w1, gate, w2)]
+    norm = lambda v, w: v / (v.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w
+    o = alpha * L[0] + torch.sigmoid(L[3]) * norm(norm(L[0], L[1]) @ wb.to(D), L[2])
+    (norm(o, L[4]) * c.to(D)).sum().backward()
+    for got, leaf in zip((dx, dw0, dw1, dgate, dw2), L):
+        # (chained fp32 steps with matrix products of 96 terms in between: each within 2^-16)
+        assert float((got.to(D) - leaf.grad).norm() / leaf.grad.norm()) <= 2.0 ** -14
