@@ -1,7 +1,8 @@
 """B200 (sm_100a) fused mixture-of-experts expert forward.
 
 The compute lives in libmoe_b200.so (C ABI: include/moe.h); this package is a
-thin ctypes binding over it plus seeded synthetic workloads.  Importing the
+thin binding over it (ctypes, and the compiled module _moe_torch for the operators
+around the forward) plus seeded synthetic workloads.  Importing the
 package does not load the library; the first call does, and raises if the
 library was not built (there is no CPU fallback).
 """

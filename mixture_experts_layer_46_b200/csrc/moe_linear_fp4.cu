@@ -11,7 +11,9 @@
 //      is read by the tensor core over the pair).  224 is the widest tile that leaves two
 //      accumulators (448 columns) and the scales (48) in the 512 columns of TMEM, so the
 //      epilogue of a tile runs under the next tile's products; a tile of 256 would read a
-//      tenth fewer bytes a product and stall for its epilogue.
+//      tenth fewer bytes a product and stall for its epilogue.  T = N = 8192, K = 4096: 106 us
+//      (5.2 PFLOP/s; 99 us with e8m0 scales), bound by the tiles' way into shared memory and out
+//      of it again: 37 KB a step each way where the products take 448 cycles.
 // One to four tokens (one launch): the weights' bytes are the work; every block quantises
 // the few rows of x into shared memory, a warp takes a weight row at a time.  The products of
 // two e2m1 numbers are multiples of 1/4 of at most 36, so eight of them add up exactly in a
