@@ -279,10 +279,12 @@ cudaError_t launch_clusters(const Route& g, cudaStream_t st) {
 
 }  // namespace
 
-// Up to four tokens take clusters of sixteen (7.4 us at one token against 9.5 with eight); with
-// more, the few places for such clusters run out (eight tokens: 10.6 against 6.6 us).
+// More CTAs a token are faster as long as the clusters find places at once: sixteen for up to four
+// tokens (7.4 us at one token, 9.5 with eight), eight for up to eight (6.7 us at eight tokens of
+// 2080 columns, 10.6 with sixteen; sixteen tokens 11.2), then four (20 to 28 tokens 6.9 us).
 cudaError_t launch_route(const Route& g, cudaStream_t st) {
-  return g.T <= 4 ? launch_clusters<16>(g, st) : launch_clusters<8>(g, st);
+  if (g.T <= 4) return launch_clusters<16>(g, st);
+  return g.T <= 8 ? launch_clusters<8>(g, st) : launch_clusters<4>(g, st);
 }
 
 }  // namespace moe
