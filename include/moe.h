@@ -544,8 +544,9 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
  * whole tensor's largest value at code 6 and scale 448):
  *   scale = e4m3(amax_16 / (6 G)),  code = e2m1(v / (scale G)),  value = code scale G
  * both rounded to nearest of the exact quotient, ties to even, saturating; a block whose scale
- * rounds to 0, and every block for G <= 0, becomes zeros.  dst's codes and scales have unit
- * inner strides.  src holds finite numbers.
+ * rounds to 0, and every block for G <= 0, becomes zeros; infinities saturate; a block with a
+ * NaN gets a NaN scale (and in moe_linear_fp4 its token's outputs are NaN).  dst's codes and
+ * scales have unit inner strides.
  *
  * moe_linear_fp4: out[t, n] = sum_k xq[t, k] wq[n, k], x quantised on the way in by the
  * weight's form:

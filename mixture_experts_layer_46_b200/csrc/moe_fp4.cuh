@@ -57,6 +57,9 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v, float f) {
   return r;
 }
 
+// A block with a NaN gets a NaN for its scale, so that whatever it meets in a product is NaN.
+constexpr uint32_t kNanE4m3 = 0x7fu, kNanE8m0 = 0xffu;
+
 constexpr float kDown = 1.0f - 1.0f / (1 << 20), kUp = 1.0f + 1.0f / (1 << 20);
 
 // e4m3 code of amax / (6 G); G a positive finite float, inv6 = 1 / (6 G), amax >= 0.
@@ -117,6 +120,7 @@ __device__ __forceinline__ void nv_codes16(const float* v, float s, float G, flo
 // low nibble), returns the scale.  inv6 = 1 / (6 G).
 __device__ __forceinline__ uint32_t nv_quant16(const float* v, float amax, float G, float inv6, uint32_t (&w)[2]) {
   w[0] = w[1] = 0u;
+  if (amax != amax) return kNanE4m3;
   if (!(G > 0.0f) || !(amax > 0.0f)) return 0u;
   const bool far = !(G > 1e-24f && G < 1e24f);
   const uint32_t sc = far ? nv_scale_far(amax, G) : nv_scale(amax, G, inv6);
@@ -134,11 +138,17 @@ __device__ __forceinline__ uint32_t nv_quant16(const float* v, float amax, float
   return sc;
 }
 
-// the largest magnitude of 16
+// the larger of two, NaN where either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// the largest magnitude of 16 (NaN with one among them)
 __device__ __forceinline__ float amax16(const float* v) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+  for (int i = 0; i < 16; ++i) m = max_nan(m, fabsf(v[i]));
   return m;
 }
 

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(256, 4) fp4_prepare_kernel(const FpPrepare g) 
           uint32_t m = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-          amax = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+          amax = max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
         } else {
           read16(g.x, g.wide, row, c, v);
           amax = amax16(v);
@@ -185,12 +185,12 @@ __global__ void __launch_bounds__(256, 4) fp4_prepare_kernel(const FpPrepare g) 
           sc = nv_quant16(v, amax, G, inv6, w);
         } else {
           // (K is a multiple of 32: both threads of a block are here)
-          amax = fmaxf(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30), amax, 1));
+          amax = max_nan(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30), amax, 1));
           const int e = mx_scale_exp(amax);
           const float f = exp2i_neg(e);
           w[0] = cvt_e2m1x8(v, f);
           w[1] = cvt_e2m1x8(v + 8, f);
-          sc = static_cast<uint32_t>(e + 127);
+          sc = amax != amax ? kNanE8m0 : static_cast<uint32_t>(e + 127);
         }
         *reinterpret_cast<uint2*>(g.codes + row * (static_cast<int64_t>(g.num_k) * 128) + (c >> 1)) = make_uint2(w[0], w[1]);
       }
@@ -597,12 +597,12 @@ __global__ void __launch_bounds__(kRowsThreads, kT <= 2 ? 4 : 2) linear_fp4_rows
     if constexpr (kNv) {
       xs[i] = e4m3x2_floats(nv_quant16(v, amax, xg, 1.0f / (6.0f * xg), w)).x;
     } else {
-      const float both = fmaxf(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30), amax, 1));
+      const float both = max_nan(amax, __shfl_xor_sync(0x3u << (threadIdx.x & 30), amax, 1));
       const int e = mx_scale_exp(both);
       const float f = exp2i_neg(e);
       w[0] = cvt_e2m1x8(v, f);
       w[1] = cvt_e2m1x8(v + 8, f);
-      if ((c16 & 1) == 0) xs[t * G + c] = exp2i_neg(-e);
+      if ((c16 & 1) == 0) xs[t * G + c] = both != both ? both : exp2i_neg(-e);
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {

@@ -236,3 +236,28 @@ def test_quantise_then_multiply():
     code = unpack(xc)
     v = GRID.cuda()[code & 7] * torch.where(code >= 8, -1.0, 1.0) * (xs.double().repeat_interleave(16, 1) * xg.double())
     check(moe.linear_fp4(x, wc, ws, x_global=xg, w_global=wg), v, nv64(w, wg)[2])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("form", ["nv", "mx"])
+@pytest.mark.parametrize("T", [2, 150])
+def test_linear_non_finite(T, form, dt):
+    """A NaN in a token makes its outputs NaN and no other's; an infinity saturates as the rule says."""
+    N, K = 72, 320
+    x = rows(1, T, K, dt)
+    codes, sf, wg, wv = weight(2, N, K, form)
+    xg = (x.float().abs().max() / 2688.0).reshape(1) if form == "nv" else None
+    clean = moe.linear_fp4(x, codes, sf, x_global=xg, w_global=wg)
+    bad = x.clone()
+    bad[1, 37] = float("nan")
+    out = moe.linear_fp4(bad, codes, sf, x_global=xg, w_global=wg)
+    assert bool(out[1].isnan().all())
+    keep = torch.arange(T, device="cuda") != 1
+    assert torch.equal(out[keep], clean[keep])
+    if form == "nv":
+        bad[1, 37] = float("inf")
+        big = bad.clone()
+        big[1, 37] = 1e30  # far beyond scale 448 and code 6: the same codes
+        assert torch.equal(moe.linear_fp4(bad, codes, sf, x_global=xg, w_global=wg),
+                           moe.linear_fp4(big, codes, sf, x_global=xg, w_global=wg))
+        assert bool(moe.quantize_nvfp4(torch.full((1, 32), float("nan"), dtype=dt, device="cuda"), xg)[1].float().isnan().all())
