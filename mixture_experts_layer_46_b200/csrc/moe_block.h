@@ -34,7 +34,7 @@ moe_status_t api_forward(const moe_tensor_t* x, const moe_w13_t* w13, const moe_
 // ---- norms (moe_norm.cu) -----------------------------------------------------
 
 constexpr int kNormMaxSms = 160;      // the gradient's workspace size is for at most this many SMs
-constexpr int64_t kNormMaxH = 16384;  // 1024 threads x 2 slots x 8 elements
+constexpr int64_t kNormMaxH = 16384;  // 1024 threads x 2 slots (or 512 x 4) x 8 elements
 
 // Rows of bf16 or fp32 elements; strides in elements (s0 = 0: the same row for every token).
 struct RowView {

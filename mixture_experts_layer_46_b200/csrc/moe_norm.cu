@@ -769,7 +769,9 @@ Shape shape_of(int64_t H, bool wide) {
   const int n = static_cast<int>((H + 7) / 8);
   // (two slots halve what a row costs besides its elements: T=16384 H=1024 after + next 41 -> 33 us;
   // through the strides, where an element is a load, one is faster: 1023 x 1407 f32 16 against 20)
-  const int vec = n <= (wide ? 64 : 256) ? 1 : 2;
+  // Rows of more than 8192 take four (512 threads; with 1024 and two the registers spill: T=4096
+  // H=16384 after + next 129 against 100 us); at H=4096 four are slower (92 against 104).
+  const int vec = n <= (wide ? 64 : 256) ? 1 : wide && n > 1024 ? 4 : 2;
   Shape s;
   s.vec = vec;
   s.threads = ((n + vec - 1) / vec + 31) / 32 * 32;
@@ -822,18 +824,22 @@ cudaError_t launch_rows(const Args& g, int threads, int64_t grid, int smem, cuda
 }
 
 // Launches K<slots, mode, threads bound> for a row of H elements.
-#define MOE_NORM_MODE(K, V, M, g, s, grid, smem, st)                                                  \
-  ((s).threads <= 256   ? launch_rows<K<V, M, 256>>(g, (s).threads, grid, smem, st)                   \
-   : (s).threads <= 512 ? launch_rows<K<2, M, 512>>(g, (s).threads, grid, smem, st)                   \
-                        : launch_rows<K<2, M, 1024>>(g, (s).threads, grid, smem, st))
-#define MOE_NORM_VEC(K, V, mode, g, s, grid, smem, st)                                                \
-  ((mode) == kStrided    ? MOE_NORM_MODE(K, V, kStrided, g, s, grid, 0, st)                           \
-   : (mode) == kWide     ? MOE_NORM_MODE(K, V, kWide, g, s, grid, 0, st)                              \
-   : (mode) == kRingBf16 ? MOE_NORM_MODE(K, V, kRingBf16, g, s, grid, smem, st)                       \
-   : (mode) == kRingF32  ? MOE_NORM_MODE(K, V, kRingF32, g, s, grid, smem, st)                        \
-                         : MOE_NORM_MODE(K, V, kRing, g, s, grid, smem, st))
+#define MOE_NORM_WIDE(K, M, g, s, grid, smem, st)                                                     \
+  ((s).vec == 1         ? launch_rows<K<1, M, 256>>(g, (s).threads, grid, smem, st)                   \
+   : (s).vec == 4       ? launch_rows<K<4, M, 512>>(g, (s).threads, grid, smem, st)                   \
+   : (s).threads <= 256 ? launch_rows<K<2, M, 256>>(g, (s).threads, grid, smem, st)                   \
+                        : launch_rows<K<2, M, 512>>(g, (s).threads, grid, smem, st))
+#define MOE_NORM_STRIDED(K, g, s, grid, st)                                                           \
+  ((s).vec == 1         ? launch_rows<K<1, kStrided, 256>>(g, (s).threads, grid, 0, st)               \
+   : (s).threads <= 256 ? launch_rows<K<2, kStrided, 256>>(g, (s).threads, grid, 0, st)               \
+   : (s).threads <= 512 ? launch_rows<K<2, kStrided, 512>>(g, (s).threads, grid, 0, st)               \
+                        : launch_rows<K<2, kStrided, 1024>>(g, (s).threads, grid, 0, st))
 #define MOE_NORM_LAUNCH(K, g, mode, s, grid, smem, st)                                                \
-  ((s).vec == 1 ? MOE_NORM_VEC(K, 1, mode, g, s, grid, smem, st) : MOE_NORM_VEC(K, 2, mode, g, s, grid, smem, st))
+  ((mode) == kStrided    ? MOE_NORM_STRIDED(K, g, s, grid, st)                                        \
+   : (mode) == kWide     ? MOE_NORM_WIDE(K, kWide, g, s, grid, 0, st)                                 \
+   : (mode) == kRingBf16 ? MOE_NORM_WIDE(K, kRingBf16, g, s, grid, smem, st)                          \
+   : (mode) == kRingF32  ? MOE_NORM_WIDE(K, kRingF32, g, s, grid, smem, st)                           \
+                         : MOE_NORM_WIDE(K, kRing, g, s, grid, smem, st))
 
 // the ring's form from the types of the stream's and the block's tensors (absent ones do not count)
 int mode_of(bool wide, int smem, std::initializer_list<const RowView*> stream, std::initializer_list<const RowView*> block) {

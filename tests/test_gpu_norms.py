@@ -54,7 +54,8 @@ def rstd64(v, eps=1e-6):
     return 1 / (v.to(D).pow(2).mean(-1) + eps).sqrt()
 
 
-SHAPES = [(1, 1), (1, 4096), (2, 7), (3, 64), (5, 1407), (33, 2048), (700, 512), (9, 4104), (3, 16384), (257, 1000)]
+SHAPES = [(1, 1), (1, 4096), (2, 7), (3, 64), (5, 1407), (33, 2048), (700, 512), (9, 4104), (3, 16384), (257, 1000),
+          (320, 16384), (310, 9000), (400, 6000)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
