@@ -799,7 +799,7 @@ int ring_of(RowRing* r, int H, int64_t T, int64_t grid, int per_sm) {
   const int64_t room = (220 << 10) / per_sm - 1024 - 128;
   int64_t n = room / r->stage_bytes;
   const int64_t want = kRingBytes / (per_sm * r->stage_bytes);
-  if (n > want) n = want < 2 ? 2 : want;
+  if (n > want && n > 2) n = want < 2 ? 2 : want;
   if (n > 8) n = 8;
   const int64_t rows = (T + grid - 1) / grid;
   if (n > rows) n = rows;
