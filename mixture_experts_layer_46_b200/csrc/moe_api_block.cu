@@ -378,10 +378,8 @@ moe_status_t moe_linear_fp4(const moe_tensor_t* x, const moe_tensor_t* weight, i
   a.os1 = out->strides[1];
   const bool rows = linear_fp4_by_rows(a.T, a.N, a.K);
   const LinearFp4Plan p = linear_fp4_plan(a.T, a.N, a.K, nv);
-  if (!rows) {
-    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
-    if (workspace_bytes < p.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  }
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < (p.total > 256 ? p.total : 256)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (a.T == 0) return MOE_OK;
   int sms = 0;
   MOE_TRY(api_device(&sms, &a.err));

@@ -2,7 +2,7 @@
 // factors e2m1 codes with a scale per block of K (e8m0 per 32, or e4m3 per 16 times one float),
 // x quantised on the way in.
 //
-// More than a few tokens (two launches):
+// Else (two launches):
 //   1. fp4_prepare: x -> codes [T, K/2] and scales, and the weight's scales, both placed in the
 //      128-row x 4-scale atoms that the tensor core reads (byte (row % 32) * 16 + (row / 32) * 4
 //      + scale), one contiguous run a k-step of 256 elements and tile.  Bound by the read of x.
@@ -14,7 +14,7 @@
 //      tenth fewer bytes a product and stall for its epilogue.  T = N = 8192, K = 4096: 106 us
 //      (5.2 PFLOP/s; 99 us with e8m0 scales), bound by the tiles' way into shared memory and out
 //      of it again: 37 KB a step each way where the products take 448 cycles.
-// One to four tokens (one launch): the weights' bytes are the work; every block quantises
+// A few tokens of a matrix that is not large (one launch): the weights' bytes are the work; every block quantises
 // the few rows of x into shared memory, a warp takes a weight row at a time.  The products of
 // two e2m1 numbers are multiples of 1/4 of at most 36, so eight of them add up exactly in a
 // half; each block of 16 is then scaled and added in fp32.
@@ -542,7 +542,7 @@ constexpr int kRowsThreads = 256;
 struct FpRows {
   RowView x;
   int wide;
-  int K, groups;           // groups: blocks of 32
+  int T, K, groups;        // groups: blocks of 32
   int64_t N;
   const float* x_global;
   const float* w_global;
@@ -554,7 +554,7 @@ struct FpRows {
   int64_t os0, os1;
 };
 
-// x in shared memory: halves [T][group of 32][4 parts of 16 bytes, turned by the group] and the
+// Four tokens a blockIdx.y.  x in shared memory: halves [T][group of 32][4 parts of 16 bytes, turned by the group] and the
 // scales of each group of 16 (kNv) or 32 as floats.
 template <bool kNv, int kT>
 __global__ void __launch_bounds__(kRowsThreads, kT <= 2 ? 4 : 2) linear_fp4_rows_kernel(const FpRows g) {
@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(kRowsThreads, kT <= 2 ? 4 : 2) linear_fp4_rows
   };
   const int64_t stride = static_cast<int64_t>(gridDim.x) * (kRowsThreads / 32);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5);
+  const int t0 = blockIdx.y * kT, nt = g.T - t0;  // (of the last four some may be missing)
   pdl_wait();
   pdl_launch_dependents();
   if (first < g.N) fetch(first, lane);  // on their way while x is quantised
@@ -591,7 +592,12 @@ __global__ void __launch_bounds__(kRowsThreads, kT <= 2 ? 4 : 2) linear_fp4_rows
   for (int i = threadIdx.x; i < kT * G * 2; i += kRowsThreads) {  // blocks of 16 (G is whole: pairs stay together)
     const int t = i / (2 * G), c16 = i - t * 2 * G, c = c16 >> 1;
     float v[16];
-    read16(g.x, g.wide, t, c16 * 16, v);
+    if (t < nt) {
+      read16(g.x, g.wide, t0 + t, c16 * 16, v);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[q] = 0.0f;
+    }
     uint32_t w[2];
     const float amax = amax16(v);
     if constexpr (kNv) {
@@ -673,7 +679,7 @@ __global__ void __launch_bounds__(kRowsThreads, kT <= 2 ? 4 : 2) linear_fp4_rows
     for (int t = 0; t < kT; ++t) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-      if (lane == 0) g.out[t * g.os0 + n * g.os1] = __float2bfloat16_rn(acc[t] * scale);
+      if (lane == 0 && t < nt) g.out[(t0 + t) * g.os0 + n * g.os1] = __float2bfloat16_rn(acc[t] * scale);
     }
   }
 }
@@ -701,7 +707,8 @@ cudaError_t launch_rows(const FpRows& r, int num_sms, cudaStream_t st) {
   if (rc != cudaSuccess) return rc;
   int64_t blocks = (r.N + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
   if (blocks > 4 * num_sms) blocks = 4 * num_sms;
-  return launch_pdl(linear_fp4_rows_kernel<kNv, kT>, dim3(static_cast<unsigned>(blocks)), dim3(kRowsThreads), smem, st, r);
+  return launch_pdl(linear_fp4_rows_kernel<kNv, kT>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((r.T + kT - 1) / kT)),
+                    dim3(kRowsThreads), smem, st, r);
 }
 
 // Weight rows of a pair's tile: the width whose waves of tiles take the fewest steps.  A step
@@ -724,10 +731,13 @@ int tile_of(int64_t T, int64_t N) {
 
 }  // namespace
 
-// Every token costs a read of x from shared memory for every weight: 4096 x 4096 takes 8.6, 11.5 and
-// 16.9 us for 1, 2 and 4 tokens, 12.6 on the pairs; a small matrix is over before two launches are.
+// By rows a call takes about 3 us and one for every 4.5 M weights times tokens; the pairs' two launches
+// 5, one for every 900 of K and one for every 5 M weights, up to a few hundred tokens.  Measured by
+// rows / on pairs: 4096 x 4096, 2 tokens 8.5 / 11.7 us; 512 x 4096, 16 tokens 9.4 / 9.4; 1024 x 2048, 16
+// tokens 10.6 / 7.3; 256 x 512, 16 tokens 2.9 / 5.5.
 bool linear_fp4_by_rows(int64_t T, int64_t N, int64_t K) {
-  return T <= (N * K <= (1 << 22) ? 4 : 2) && T * (K / 32) * 72 <= static_cast<int64_t>(kRowsSmemMax);
+  return T <= 16 && (T - 1) * N * K <= (8 << 20) + 5120 * K &&
+         (T < 4 ? T : 4) * (K / 32) * 72 <= static_cast<int64_t>(kRowsSmemMax);
 }
 
 LinearFp4Plan linear_fp4_plan(int64_t T, int64_t N, int64_t K, bool nv) {
@@ -752,6 +762,7 @@ cudaError_t launch_linear_fp4_rows(const LinearFp4& a, int num_sms, cudaStream_t
   FpRows r = {};
   r.x = a.x;
   r.wide = a.wide;
+  r.T = static_cast<int>(a.T);
   r.K = static_cast<int>(a.K);
   r.groups = static_cast<int>(a.K / 32);
   r.N = a.N;
@@ -765,7 +776,7 @@ cudaError_t launch_linear_fp4_rows(const LinearFp4& a, int num_sms, cudaStream_t
   r.out = a.out;
   r.os0 = a.os0;
   r.os1 = a.os1;
-  switch (a.T * 2 + (a.nv ? 1 : 0)) {
+  switch ((a.T < 4 ? a.T : 4) * 2 + (a.nv ? 1 : 0)) {
     case 2: return launch_rows<false, 1>(r, num_sms, st);
     case 3: return launch_rows<true, 1>(r, num_sms, st);
     case 4: return launch_rows<false, 2>(r, num_sms, st);
