@@ -24,6 +24,7 @@ __device__ __forceinline__ void acc_bf16x8(float (&a)[8], const uint4& v) {
 // Every thread reads the token's k row indices itself (the same k words for
 // the whole CTA, served by L1), so there is no block barrier, and up to 8 row
 // loads of a chunk are issued back to back before they are summed (in j order).
+template <bool kFinish>  // (the plain combine keeps its registers)
 __global__ void __launch_bounds__(256) combine_kernel(const __nv_bfloat16* __restrict__ y,
                                                       const int32_t* __restrict__ inv, int64_t T,
                                                       int64_t H, int64_t k,
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __nv_bfloat16* __res
         const int32_t r = __ldg(rows + j);
         if (r >= 0) acc_bf16x8(a, __ldg(reinterpret_cast<const uint4*>(y + static_cast<int64_t>(r) * H) + c));
       }
-      if (finish8(finish, t, H, c * 8, a)) continue;
+      if (kFinish && finish8(finish, t, H, c * 8, a)) continue;
       if (vec_out) {
         uint4 o;
         o.x = pack_bf16x2(a[0], a[1]);
@@ -80,8 +81,12 @@ cudaError_t launch_combine(const __nv_bfloat16* y, const int32_t* inv, int64_t T
   int64_t blocks = T < 65535 ? T : 65535;
   if (blocks < 1) blocks = 1;
   if (launches) *launches += 1;
-  return launch_pdl(combine_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, y, inv,
-                    T, H, k, static_cast<__nv_bfloat16*>(out), os0, os1, vec_out, finish);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if (finish.mode != kFinishNone)
+    return launch_pdl(combine_kernel<true>, grid, dim3(256), 0, st, y, inv, T, H, k, static_cast<__nv_bfloat16*>(out),
+                      os0, os1, vec_out, finish);
+  return launch_pdl(combine_kernel<false>, grid, dim3(256), 0, st, y, inv, T, H, k, static_cast<__nv_bfloat16*>(out), os0,
+                    os1, vec_out, finish);
 }
 
 }  // namespace moe
