@@ -12,8 +12,8 @@
 //      accumulators (448 columns) and the scales (48) in the 512 columns of TMEM, so the
 //      epilogue of a tile runs under the next tile's products; a tile of 256 would read a
 //      tenth fewer bytes a product and stall for its epilogue.  T = N = 8192, K = 4096: 106 us
-//      (5.2 PFLOP/s; 99 us with e8m0 scales), bound by the tiles' way into shared memory and out
-//      of it again: 37 KB a step each way where the products take 448 cycles.
+//      (5.2 PFLOP/s; 99 us with e8m0 scales): the products 81, the copies of the scales into
+//      tensor memory between them 16 (twelve a k-step, about 8 cycles each), loads 9, stores 7.
 // A few tokens of a matrix that is not large (one launch): the weights' bytes are the work; every block quantises
 // the few rows of x into shared memory, a warp takes a weight row at a time.  The products of
 // two e2m1 numbers are multiples of 1/4 of at most 36, so eight of them add up exactly in a
@@ -128,8 +128,9 @@ struct FpPrepare {
 
 // Blocks of 16 x 16 threads.  The first x_blocks walk over tiles of 16 rows x 256 elements of x,
 // a thread 16 neighbours of a row, the next tile's on their way while the last ones are quantised;
-// the others place the weight's scales.  T = 8192, K = 4096: 23 us, the instructions of the two
-// roundings and the ties bound it (e8m0 scales 17 us; reading x and writing the codes 13 us).  kFast: bf16, 16-byte loads.
+// the others place the weight's scales.  kFast: bf16, 16-byte loads.  T = 8192, K = 4096: 23 us, 21 of
+// them without the arithmetic (reading x and writing the codes would take 13); more rows on their
+// way at once, or whole rows a block, were slower (32 and 24.5 us).
 template <bool kNv, bool kFast>
 __global__ void __launch_bounds__(256, 4) fp4_prepare_kernel(const FpPrepare g) {
   constexpr int kAtoms = atoms_per_step<kNv>();
