@@ -809,7 +809,7 @@ int ring_of(RowRing* r, int H, int64_t T, int64_t grid, int per_sm) {
 
 template <auto kKernel, typename Args>
 cudaError_t launch_rows(const Args& g, int threads, int64_t grid, int smem, cudaStream_t st) {
-  if (smem > (48 << 10)) {
+  if (smem > 0) {  // (the 48 KB that need no raised limit hold the kernel's own shared memory too)
     static std::atomic<unsigned long long> configured{0};  // devices whose limit is raised already
     int dev = 0;
     cudaError_t rc = cudaGetDevice(&dev);

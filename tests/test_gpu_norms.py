@@ -11,6 +11,10 @@ Tolerances, with u = 2^-24 (fp32) and h = half a step of the output's type (bf16
     2^-18: (2^-18 + (T + 64) u) sum|term| + h |ref|.
 """
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -364,3 +368,22 @@ def test_a_block_as_it_trains():
     for got, leaf in zip((dx, dw0, dw1, dgate, dw2), L):
         # (chained fp32 steps with matrix products of 96 terms in between: each within 2^-16)
         assert float((got.to(D) - leaf.grad).norm() / leaf.grad.norm()) <= 2.0 ** -14
+
+
+def test_rings_between_the_default_and_the_raised_limit():
+    """Rows whose ring just fills the 48 KB that a launch may have without asking (the kernel's own
+    shared memory is part of them), in a process that has not asked for more yet."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = """
+import test_gpu_norms as t
+for T, H in [(700, 4880), (4096, 3056), (4096, 4080)]:
+    t.test_before(T, H, t.BF, t.BF, t.BF)
+for T, H in [(700, 4080), (700, 4072), (4096, 3056)]:
+    t.test_after(T, H, "none", "none", t.BF, t.BF, True, 1.0)
+    t.test_after_backward(T, H, "channel", "sigmoid", t.BF, t.BF, True, t.F32)
+for T, H in [(700, 2712), (700, 4080)]:
+    t.test_before_backward(T, H, t.BF, t.BF, 1.0)
+"""
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
