@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr size_t kOptInSmem = 47 * 1024;  // a launch has 48 KB unasked, the kernel's static arrays among them
 constexpr int kSmallGroups = kAlignSmallMax / kThreads;  // 32-slot groups per warp, one CTA
 constexpr int kChunkGroups = kAlignChunk / kThreads;     // 32-slot groups per warp, per chunk
 static_assert(kAlignSmallMax % kThreads == 0 && kAlignChunk % kThreads == 0, "align tiling");
@@ -558,7 +559,7 @@ cudaError_t launch_align(const View2& ids, int64_t T, int64_t k, int64_t E, int3
   cudaError_t rc;
   if (S <= kAlignSmallMax) {
     const size_t smem = sizeof(int) * (E * (kWarps + 3) + 2);
-    if (smem > 48 * 1024) {
+    if (smem > kOptInSmem) {
       rc = cudaFuncSetAttribute(align_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem);
       if (rc != cudaSuccess) return rc;
@@ -569,7 +570,7 @@ cudaError_t launch_align(const View2& ids, int64_t T, int64_t k, int64_t E, int3
     return rc;
   }
   const size_t smem_count = sizeof(int) * E * (kWarps + 1);
-  if (smem_count > 48 * 1024) {
+  if (smem_count > kOptInSmem) {
     rc = cudaFuncSetAttribute(align_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)smem_count);
     if (rc != cudaSuccess) return rc;

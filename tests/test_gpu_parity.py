@@ -577,3 +577,13 @@ def test_decode_one_kernel_repeated_calls_and_fallback_for_strided_x():
     assert torch.equal(got, unsplit)
     ref = run_oracle(cs)
     assert rel_err(first, ref) <= BF16_TOL and rel_err(unsplit, ref) <= BF16_TOL
+
+
+@pytest.mark.parametrize("E", [350, 351, 352, 371, 372, 373])
+@pytest.mark.parametrize("T", [20, 3000])
+def test_expert_counts_between_the_default_and_the_raised_shared_memory_limit(E, T):
+    """Expert counts for which the align step's tables just fill the 48 KB that a launch may have
+    without asking (the kernel's own shared memory is part of them)."""
+    case = make_case(T, 128, 64, E, 2, seed=E)
+    got = run_gpu(to_cuda(case))
+    assert rel_err(got, run_oracle(case)) <= BF16_TOL
