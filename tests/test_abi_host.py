@@ -307,3 +307,21 @@ def test_router_argument_errors_before_launch():
                              torch.zeros(2, 33)) == 1          # more than 32 columns
     assert moe.router_status(torch.zeros(0, 16), 2, 1, 0, torch.zeros(0, 2, dtype=torch.int32),
                              torch.zeros(0, 2)) == 0           # no tokens: nothing to do
+
+
+def test_scale_tensors_are_bytes_and_cover_the_codes():
+    """Scales held in a wider type are the bytes they consist of; too few of them, or e4m3 ones (per 16,
+    another format), are refused."""
+    codes = torch.zeros(3, 8, 64, dtype=torch.uint8)                # 128 elements a row: 4 scales
+    raw = torch.zeros(3, 8, 8, dtype=torch.uint8)
+    plain = moe.desc(codes, raw[:, :, :4].contiguous())
+    for wide in (torch.int32, torch.int16, torch.float8_e8m0fnu):
+        d = moe.desc(codes, raw[:, :, :4].contiguous().view(wide))
+        assert list(d.scale_strides) == list(plain.scale_strides) and list(d.sizes) == list(plain.sizes)
+    assert list(moe.desc(codes, raw).scale_strides)[:3] == [64, 8, 1]  # rows with room behind them
+    assert list(moe.desc(codes, raw.view(torch.int64)).scale_strides)[:3] == [64, 8, 1]
+    for bad in (raw[:, :, :3], raw[:, :7], raw[:2], raw[0], raw[:, :, :4].contiguous().view(torch.int32)[:, :7]):
+        with pytest.raises(ValueError, match="scales of shape"):
+            moe.desc(codes, bad)
+    with pytest.raises(ValueError, match="e4m3"):
+        moe.desc(codes, raw.view(torch.float8_e4m3fn))
