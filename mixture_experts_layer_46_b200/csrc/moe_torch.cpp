@@ -165,6 +165,44 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return nullptr;
 }
 
+void packed_codes(const at::Tensor& codes) {
+  if (codes.scalar_type() != at::kByte && codes.scalar_type() != at::ScalarType::Float4_e2m1fn_x2)
+    value_error(std::string("codes of type ") + at::toString(codes.scalar_type()) + ", not uint8 or float4_e2m1fn_x2");
+}
+bool e8m0_type(at::ScalarType t) { return t == at::kByte || t == at::ScalarType::Float8_e8m0fnu; }
+std::string shape_of(const at::Tensor& t) {
+  std::string s = "[";
+  for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
+  return s + "]";
+}
+
+// the scale format of a code matrix, from its scales' type; checks both tensors' sizes
+int32_t code_form(const at::Tensor& codes, const at::Tensor& scale) {
+  packed_codes(codes);
+  if (codes.dim() != 2 || scale.dim() != 2)
+    value_error("codes of " + std::to_string(codes.dim()) + " and scales of " + std::to_string(scale.dim()) +
+                " dimensions, not 2");
+  const bool nv = scale.scalar_type() == at::ScalarType::Float8_e4m3fn;
+  if (!nv && !e8m0_type(scale.scalar_type()))
+    value_error(std::string("scales of type ") + at::toString(scale.scalar_type()) +
+                ": float8_e4m3fn per 16, or uint8 / float8_e8m0fnu per 32");
+  const int64_t N = codes.size(0), K = 2 * codes.size(1);
+  if (K % 32 != 0 || scale.size(0) != N || scale.size(1) != K / (nv ? 16 : 32))
+    value_error("scales of shape " + shape_of(scale) + " for codes of " + std::to_string(N) + " rows of " +
+                std::to_string(K) + " elements");
+  return nv ? MOE_SCALE_E4M3_16 : MOE_SCALE_E8M0_32;
+}
+
+// the experts' codes and their e8m0 scales, one per 32 elements
+void expert_scales(const at::Tensor& codes, const at::Tensor& scale) {
+  packed_codes(codes);
+  if (!e8m0_type(scale.scalar_type()))
+    value_error(std::string("expert scales of type ") + at::toString(scale.scalar_type()) + ": uint8 / float8_e8m0fnu per 32");
+  if (codes.dim() != 3 || scale.dim() != 3 || scale.size(0) != codes.size(0) || scale.size(1) != codes.size(1) ||
+      scale.size(2) * 16 != codes.size(2))
+    value_error("expert scales of shape " + shape_of(scale) + " for codes of shape " + shape_of(codes));
+}
+
 // x, weight, eps, out, out_dtype, rstd
 PyObject* norm_before(PyObject* const* a) {
   const at::Tensor &x = *tensor(a[0], "x", true), *w = tensor(a[1], "weight");
@@ -263,6 +301,7 @@ PyObject* layer_decode(PyObject* const* a) {
   const float eps = number(a[7]), alpha = number(a[14]);
   rows(x, "x");
   rows(router, "router");
+  if (s2) expert_scales(w2, *s2);
   if (k < 1 || k > 32) value_error("k " + std::to_string(k) + ": 1 to 32");
   const Call c(x, {&router, &w2, s2, pre, post, gate, ot, it, wt, wst});
   const int64_t T = x.size(0), H = x.size(1), kk = k + shared;
@@ -279,24 +318,6 @@ PyObject* layer_decode(PyObject* const* a) {
   check(moe_layer_decode(dx.p, dpre.p, eps, drouter.p, k, renorm, shared, w13, d2.p, post_norm, dpost.p, dgate.p, act,
                          alpha, dids.p, dwts.p, dout.p, ws, n, c.stream), "moe_layer_decode");
   return pack({&out, &ids, &wts});
-}
-
-// the scale format of a code matrix, from its scales' type; checks both tensors' sizes
-int32_t code_form(const at::Tensor& codes, const at::Tensor& scale) {
-  if (codes.scalar_type() != at::kByte && codes.scalar_type() != at::ScalarType::Float4_e2m1fn_x2)
-    value_error(std::string("codes of type ") + at::toString(codes.scalar_type()) + ", not uint8 or float4_e2m1fn_x2");
-  if (codes.dim() != 2 || scale.dim() != 2)
-    value_error("codes of " + std::to_string(codes.dim()) + " and scales of " + std::to_string(scale.dim()) +
-                " dimensions, not 2");
-  const bool nv = scale.scalar_type() == at::ScalarType::Float8_e4m3fn;
-  if (!nv && scale.scalar_type() != at::kByte && scale.scalar_type() != at::ScalarType::Float8_e8m0fnu)
-    value_error(std::string("scales of type ") + at::toString(scale.scalar_type()) +
-                ": float8_e4m3fn per 16, or uint8 / float8_e8m0fnu per 32");
-  const int64_t N = codes.size(0), K = 2 * codes.size(1);
-  if (K % 32 != 0 || scale.size(0) != N || scale.size(1) != K / (nv ? 16 : 32))
-    value_error("scales of shape [" + std::to_string(scale.size(0)) + ", " + std::to_string(scale.size(1)) +
-                "] for codes of " + std::to_string(N) + " rows of " + std::to_string(K) + " elements");
-  return nv ? MOE_SCALE_E4M3_16 : MOE_SCALE_E8M0_32;
 }
 
 // x, weight, weight_scale, x_global, w_global, out, workspace

@@ -255,3 +255,22 @@ def test_layer_workspace():
     assert moe.layer_decode_workspace_bytes(2, 16416, 32, 4, 2) == 0
     with pytest.raises(ValueError, match="CUDA"):
         moe.layer_decode(rows(2), rows(4), moe.w13_from_packed(torch.zeros(4, 64, 64, dtype=BF)), torch.zeros(4, 64, 32, dtype=BF), 2)
+
+
+def test_layer_wrapper_checks_the_scales():
+    """w2's codes and scales by type and shape: e4m3 scales per 16, or too few, are not read as e8m0 per 32."""
+    w13 = moe.w13_from_packed(torch.zeros(4, 512, 128, dtype=U8), torch.zeros(4, 512, 8, dtype=U8))
+    codes = torch.zeros(4, 256, 128, dtype=U8)
+    call = lambda w2, s: moe.layer_decode(rows(2, 256), rows(4, 256), w13, w2, 2, w2_scale=s)
+    for s in (torch.zeros(4, 256, 16, dtype=U8).view(torch.float8_e4m3fn), torch.zeros(4, 256, 8),
+              torch.zeros(4, 256, 8, dtype=U8).view(torch.float8_e4m3fn)):
+        with pytest.raises(ValueError, match="type"):
+            call(codes, s)
+    for s in (torch.zeros(4, 256, 7, dtype=U8), torch.zeros(4, 255, 8, dtype=U8), torch.zeros(256, 8, dtype=U8),
+              torch.zeros(4, 256, 16, dtype=U8), torch.zeros(3, 256, 8, dtype=U8)):
+        with pytest.raises(ValueError, match="shape"):
+            call(codes, s)
+    with pytest.raises(ValueError, match="codes of type"):
+        call(torch.zeros(4, 256, 128, dtype=BF), torch.zeros(4, 256, 8, dtype=U8))
+    with pytest.raises(ValueError, match="CUDA"):
+        call(codes, torch.zeros(4, 256, 8, dtype=U8))
