@@ -33,6 +33,13 @@ const at::Tensor* tensor(PyObject* o, const char* name, bool required = false) {
   return &THPVariable_Unpack(o);
 }
 
+// a caller's workspace: one block of memory, so that its element count is that of the bytes behind its address
+const at::Tensor* scratch(PyObject* o) {
+  const at::Tensor* t = tensor(o, "workspace");
+  if (t && !t->is_contiguous()) value_error("workspace is not contiguous");
+  return t;
+}
+
 at::ScalarType dtype_or(PyObject* o, at::ScalarType other) {
   if (o == Py_None) return other;
   if (!THPDtype_Check(o)) value_error("a dtype is not a torch.dtype");
@@ -245,7 +252,7 @@ PyObject* norm_before_backward(PyObject* const* a) {
   const at::Tensor &d = *tensor(a[0], "dout", true), &x = *tensor(a[1], "x", true), &r = *tensor(a[2], "rstd", true);
   const at::Tensor *w = tensor(a[3], "weight"), *res = tensor(a[4], "residual_grad");
   const float alpha = number(a[5]);
-  const at::Tensor *dxt = tensor(a[6], "dx"), *dwt = tensor(a[7], "dweight"), *wst = tensor(a[10], "workspace");
+  const at::Tensor *dxt = tensor(a[6], "dx"), *dwt = tensor(a[7], "dweight"), *wst = scratch(a[10]);
   const bool want = dwt || (w && PyObject_IsTrue(a[8]) == 1);
   rows(d, "dout");
   const Call c(d, {&x, &r, w, res, dxt, dwt, wst});
@@ -269,7 +276,7 @@ PyObject* norm_after_backward(PyObject* const* a) {
   const at::Tensor *r = tensor(a[2], "rstd"), *w = tensor(a[3], "weight"), *g = tensor(a[4], "gate");
   const int32_t act = integer(a[5]), normalize = integer(a[6]);
   const at::Tensor *dyt = tensor(a[7], "dy"), *dwt = tensor(a[8], "dweight"), *dgt = tensor(a[9], "dgate"),
-                   *wst = tensor(a[13], "workspace");
+                   *wst = scratch(a[13]);
   const bool want_w = dwt || (w && PyObject_IsTrue(a[10]) == 1), want_g = dgt || (g && PyObject_IsTrue(a[11]) == 1);
   rows(d, "dout");
   const Call c(d, {&y, r, w, g, dyt, dwt, dgt, wst});
@@ -295,7 +302,7 @@ PyObject* layer_decode(PyObject* const* a) {
   if (!w13 && PyErr_Occurred()) throw Raised{};
   const at::Tensor *s2 = tensor(a[4], "w2_scale"), *pre = tensor(a[6], "pre_weight"), *post = tensor(a[11], "post_weight"),
                    *gate = tensor(a[12], "gate"), *ot = tensor(a[15], "out"), *it = tensor(a[16], "topk_ids"),
-                   *wt = tensor(a[17], "topk_weights"), *wst = tensor(a[18], "workspace");
+                   *wt = tensor(a[17], "topk_weights"), *wst = scratch(a[18]);
   const int32_t k = integer(a[5]), renorm = integer(a[8]), shared = integer(a[9]), post_norm = integer(a[10]),
                 act = integer(a[13]);
   const float eps = number(a[7]), alpha = number(a[14]);
@@ -324,7 +331,7 @@ PyObject* layer_decode(PyObject* const* a) {
 PyObject* linear_fp4(PyObject* const* a) {
   const at::Tensor &x = *tensor(a[0], "x", true), &w = *tensor(a[1], "weight", true), &s = *tensor(a[2], "weight_scale", true);
   const at::Tensor *xg = tensor(a[3], "x_global"), *wg = tensor(a[4], "w_global"), *ot = tensor(a[5], "out"),
-                   *wst = tensor(a[6], "workspace");
+                   *wst = scratch(a[6]);
   rows(x, "x");
   const int32_t form = code_form(w, s);
   const Call c(x, {&w, &s, xg, wg, ot, wst});

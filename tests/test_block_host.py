@@ -274,3 +274,16 @@ def test_layer_wrapper_checks_the_scales():
         call(torch.zeros(4, 256, 128, dtype=BF), torch.zeros(4, 256, 8, dtype=U8))
     with pytest.raises(ValueError, match="CUDA"):
         call(codes, torch.zeros(4, 256, 8, dtype=U8))
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(1, dtype=U8).expand(1 << 24), torch.zeros(1 << 22, dtype=U8)[::2]])
+def test_wrappers_refuse_workspaces_that_are_not_one_block_of_memory(ws):
+    """Their element count says nothing of the bytes behind their address."""
+    x, r, w = rows(), torch.zeros(4), torch.zeros(64)
+    w13 = moe.w13_from_packed(torch.zeros(4, 64, 64, dtype=BF))
+    for call in (lambda: moe.norm_before_backward(x, x, r, w, workspace=ws),
+                 lambda: moe.norm_after_backward(x, x, r, w, workspace=ws),
+                 lambda: moe.layer_decode(x, rows(4), w13, torch.zeros(4, 64, 32, dtype=BF), 2, workspace=ws),
+                 lambda: moe.linear_fp4(x, torch.zeros(48, 32, dtype=U8), torch.zeros(48, 2, dtype=U8), workspace=ws)):
+        with pytest.raises(ValueError, match="contiguous"):
+            call()
