@@ -136,6 +136,12 @@ int32_t integer(PyObject* o) {
   return static_cast<int32_t>(v);
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v != 0;
+}
+
 PyObject* pack(std::initializer_list<const at::Tensor*> ts) {
   PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
   if (!r) throw Raised{};
@@ -232,7 +238,7 @@ PyObject* norm_after(PyObject* const* a) {
   const float alpha = number(a[6]), eps = number(a[7]);
   const at::Tensor *o = tensor(a[8], "out"), *rs = tensor(a[10], "rstd"), *wn = tensor(a[12], "next_weight"),
                    *no = tensor(a[13], "next_out"), *nr = tensor(a[15], "next_rstd");
-  const bool next = a[11] == Py_None ? (wn || no || nr) : PyObject_IsTrue(a[11]) == 1;
+  const bool next = a[11] == Py_None ? (wn || no || nr) : truth(a[11]);
   rows(y, "y");
   const Call c(y, {x, w, g, o, rs, wn, no, nr});
   const at::Tensor out = c.given(o, y.sizes(), dtype_or(a[9], (x ? x : &y)->scalar_type()));
@@ -253,7 +259,7 @@ PyObject* norm_before_backward(PyObject* const* a) {
   const at::Tensor *w = tensor(a[3], "weight"), *res = tensor(a[4], "residual_grad");
   const float alpha = number(a[5]);
   const at::Tensor *dxt = tensor(a[6], "dx"), *dwt = tensor(a[7], "dweight"), *wst = scratch(a[10]);
-  const bool want = dwt || (w && PyObject_IsTrue(a[8]) == 1);
+  const bool want = dwt || (w && truth(a[8]));
   rows(d, "dout");
   const Call c(d, {&x, &r, w, res, dxt, dwt, wst});
   const at::Tensor dx = c.given(dxt, d.sizes(), x.scalar_type());
@@ -277,7 +283,7 @@ PyObject* norm_after_backward(PyObject* const* a) {
   const int32_t act = integer(a[5]), normalize = integer(a[6]);
   const at::Tensor *dyt = tensor(a[7], "dy"), *dwt = tensor(a[8], "dweight"), *dgt = tensor(a[9], "dgate"),
                    *wst = scratch(a[13]);
-  const bool want_w = dwt || (w && PyObject_IsTrue(a[10]) == 1), want_g = dgt || (g && PyObject_IsTrue(a[11]) == 1);
+  const bool want_w = dwt || (w && truth(a[10])), want_g = dgt || (g && truth(a[11]));
   rows(d, "dout");
   const Call c(d, {&y, r, w, g, dyt, dwt, dgt, wst});
   const at::ScalarType type = dtype_or(a[12], at::kFloat);

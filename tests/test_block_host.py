@@ -287,3 +287,13 @@ def test_wrappers_refuse_workspaces_that_are_not_one_block_of_memory(ws):
                  lambda: moe.linear_fp4(x, torch.zeros(48, 32, dtype=U8), torch.zeros(48, 2, dtype=U8), workspace=ws)):
         with pytest.raises(ValueError, match="contiguous"):
             call()
+
+
+def test_wrappers_pass_on_what_a_truth_value_raises():
+    """A flag whose truth value raises is that error, not a false flag."""
+    x, r, w, many = rows(), torch.zeros(4), torch.zeros(64), torch.zeros(2)
+    for call in (lambda: moe.norm_after(x, next_norm=many), lambda: moe.norm_before_backward(x, x, r, w, weight_grad=many),
+                 lambda: moe.norm_after_backward(x, x, r, w, weight_grad=many),
+                 lambda: moe.norm_after_backward(x, x, r, w, torch.zeros(1, 64), gate_grad=many)):
+        with pytest.raises(RuntimeError, match="[Bb]oolean value"):
+            call()
