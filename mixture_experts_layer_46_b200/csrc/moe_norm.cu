@@ -687,6 +687,7 @@ __global__ void __launch_bounds__(kMaxThreads, min_blocks(kResident, kMaxThreads
     }
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
+      if (!g.normalize) y[v] = Vec8();  // (dy does not depend on y, its infinities and NaNs included)
       axpy8(d[v], -c, y[v]);
       scale8(d[v], r);
       store8<kMode>(g.dy, block_type<kMode>(g.dy), t, v, g.H, d[v]);

@@ -387,3 +387,17 @@ for T, H in [(700, 2712), (700, 4080)]:
     env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
     r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("T,H", [(4, 64), (5, 33), (900, 512), (400, 16384)])
+@pytest.mark.parametrize("gate,act", [("none", "none"), ("full", "tanh"), ("channel", "sigmoid"), ("token", "sigmoid"),
+                                      ("one", "none")])
+def test_without_the_norm_the_gradient_of_y_does_not_read_y(T, H, gate, act):
+    """normalize=False: dy is dout times gate and weight, whatever y holds."""
+    g = torch.Generator().manual_seed(T + 3 * H)
+    do, y, w, gt = rnd(g, T, H), rnd(g, T, H), rnd(g, H), gate_of(g, gate, T, H, BF)
+    y[1, 5], y[2, 7], y[3, 0] = float("inf"), float("nan"), -float("inf")
+    dy, _, _ = moe.norm_after_backward(do, y, None, w, gt, gate_act=act, normalize=False)
+    ref = do.to(D) * w.to(D) * (1.0 if gt is None else act64(gt, act))
+    assert bool(dy.isfinite().all())
+    within(dy, ref, 2.0 ** -18 * ref.abs())
