@@ -518,9 +518,12 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
  * Kernels: the way in (norm, router, choice); the experts, with bf16 weights and few tokens two
  * kernels over their rows with xn and h in fp32, else the kernels of moe_forward; the gate and the
  * residual are part of the last one, with post_norm = 1 or MXFP4 weights a kernel of their own.
- * NaN logits rank below every number.  Calls that take moe_forward's one-kernel decode (at most 32
- * slots, MXFP4 weights or more tokens than the kernels over rows take) must not overlap on the GPU,
- * as moe_forward_host_ws says; others may, with a workspace each.  Asynchronous on `stream`, no allocation.  T = 0 is a no-op. */
+ * Logits that are not finite (an infinity or a NaN in x's row, pre_weight or the router's row)
+ * rank below every number and count as NaN in a softmax over all experts; with finite inputs the sum of
+ * |x pre_weight router| over a row has to stay below 2^126.  Calls that take moe_forward's one-kernel
+ * decode (at most 32 slots, MXFP4 weights or more tokens than the kernels over rows take) must not
+ * overlap on the GPU, as moe_forward_host_ws says; others may, with a workspace each.  Asynchronous
+ * on `stream`, no allocation.  T = 0 is a no-op. */
 enum { MOE_LAYER_MAX_TOKENS = 32 };
 
 size_t moe_layer_decode_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int32_t wdtype);

@@ -84,9 +84,11 @@ __device__ __forceinline__ double warp_sums8(double (&v)[8]) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// A signed key that orders as the double it came from, NaN below every number (-0 is +0), and back.
+// A signed key that orders as the double it came from (-0 is +0), and back.  What is not finite comes back
+// as NaN and is below every number: the compensated sums make NaN of an infinite term, and the sums
+// in 64 bits, which would keep it, have to rank the same experts first.
 __device__ __forceinline__ long long key_of(double v) {
-  if (v != v) return (-9223372036854775807ll - 1);
+  if (!isfinite(v)) return (-9223372036854775807ll - 1);
   const long long b = __double_as_longlong(v + 0.0);
   return b ^ ((b >> 63) & 0x7fffffffffffffffll);
 }

@@ -276,3 +276,26 @@ def test_an_infinite_router_row_ranks_last():
     logits[:, 3] = -float("inf")  # inf * x carries its rounding along as NaN, which ranks below every number
     want = torch.sort(logits, dim=-1, descending=True, stable=True)[1][:, :7]
     assert torch.equal(ids.long(), want)
+
+
+@pytest.mark.parametrize("layout", ["bf16", "bf16_unaligned", "f32"])
+@pytest.mark.parametrize("T", [2, 7, 12])
+def test_logits_that_are_not_finite_rank_last_in_every_layout(T, layout):
+    """A router row with an infinity or a NaN ranks below every number, whichever way the router is read."""
+    H, E = 256, 12
+    s = make(53, T, H, 64, E)
+    s["router"][3, 7], s["router"][5, 8], s["router"][9, 9] = float("inf"), float("nan"), -float("inf")
+    router = s["router"]
+    if layout == "f32":
+        router = router.float()
+    elif layout == "bf16_unaligned":
+        router = torch.zeros(E, H + 3, dtype=BF, device="cuda")[:, :H].copy_(router)
+    out, ids, p = moe.layer_decode(s["x"], router, moe.w13_from_packed(s["w13"]), s["w2"], 8)
+    finite = [e for e in range(E) if e not in (3, 5, 9)]
+    _, wi, wp = route64(s["x"], None, s["router"][finite], 8, True, False)
+    assert torch.equal(ids.long(), torch.tensor(finite, device="cuda")[wi])
+    assert bool(((p.to(D) - wp).abs() <= 2.0 ** -20 * wp).all())
+    assert bool(out.isfinite().all())
+    # with more experts wanted than are finite, the others follow in the order of their indices
+    _, ids, _ = moe.layer_decode(s["x"], router, moe.w13_from_packed(s["w13"]), s["w2"], E)
+    assert bool((ids[:, 9:] == torch.tensor([3, 5, 9], dtype=torch.int32, device="cuda")).all())
