@@ -138,7 +138,12 @@ __device__ __forceinline__ uint32_t nv_quant16(const float* v, float amax, float
   return sc;
 }
 
-// the larger of two, NaN where either is
+// the smaller and the larger of two, NaN where either is
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));

@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kRowsThreads, kT <= 2 ? 4 : 2) linear_fp4_rows
           ws[0] = s.x;
           ws[1] = s.y;
         } else {
-          ws[0] = ws[1] = exp2i_neg(127 - static_cast<int>(sv[u]));
+          ws[0] = ws[1] = sv[u] == kNanE8m0 ? __uint_as_float(0x7fffffffu) : exp2i_neg(127 - static_cast<int>(sv[u]));
         }
         __half2 wh[16];
 #pragma unroll
@@ -671,8 +671,9 @@ __global__ void __launch_bounds__(kRowsThreads, kT <= 2 ? 4 : 2) linear_fp4_rows
           }
           if (kNv)
             acc[t] += part[0] * (xs[2 * i] * ws[0]) + part[1] * (xs[2 * i + 1] * ws[1]);
-          else
-            acc[t] += (part[0] + part[1]) * (xs[i] * ws[0]);
+          else  // (the smaller scale first: the scales' product can leave fp32's range where the term does not,
+                // and a sum times the smaller one is exact, being a multiple of 2^-129)
+            acc[t] = fmaf((part[0] + part[1]) * min_nan(xs[i], ws[0]), max_nan(xs[i], ws[0]), acc[t]);
         }
       }
     }

@@ -262,3 +262,36 @@ def test_linear_non_finite(T, form, dt):
         assert torch.equal(moe.linear_fp4(bad, codes, sf, x_global=xg, w_global=wg),
                            moe.linear_fp4(big, codes, sf, x_global=xg, w_global=wg))
         assert bool(moe.quantize_nvfp4(torch.full((1, 32), float("nan"), dtype=dt, device="cuda"), xg)[1].float().isnan().all())
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 40, 300])
+def test_linear_nan_scale_in_the_weight(T):
+    """The e8m0 code 255 is NaN: every token's output of that weight row is, in both forms of the
+    kernel, and no other."""
+    N, K = 72, 320
+    x = rows(1, T, K)
+    codes, sf, _, _ = weight(2, N, K, "mx")
+    clean = moe.linear_fp4(x, codes, sf)
+    sf[5, 3] = 255
+    out = moe.linear_fp4(x, codes, sf)
+    assert bool(out[:, 5].isnan().all())
+    keep = torch.arange(N, device="cuda") != 5
+    assert torch.equal(out[:, keep], clean[:, keep])
+
+
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("ex,ew", [(100, 100), (125, -60), (-100, 90), (-127, 120), (-60, -50), (120, -127)])
+def test_linear_far_scales(T, ex, ew):
+    """Scales whose product, or either with a partial sum, leaves fp32's range: a block whose products
+    cancel adds nothing, and the others are exact powers of two times their sums."""
+    K = 64
+    codes = torch.full((2, K // 2), 0xA2, dtype=torch.uint8, device="cuda")  # 1, -1, 1, -1, ...: cancels
+    codes[1] = 0x22
+    codes[1, 16:] = 0                                                        # row 1: 32 ones, then zeros
+    sf = torch.full((2, 2), ew + 127, dtype=torch.uint8, device="cuda")
+    x = torch.full((T, K), 4.0, dtype=F32, device="cuda") * 2.0 ** max(ex, -126)
+    x *= 2.0 ** (ex - max(ex, -126))                                         # scale 2^ex, code 4 = the sixth
+    out = moe.linear_fp4(x, codes, sf)
+    assert bool((out[:, 0] == 0).all())
+    want = torch.tensor(128.0, dtype=D) * 2.0 ** (ex + ew)
+    assert bool((out[:, 1].cpu() == want.to(BF)).all())
