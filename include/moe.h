@@ -361,8 +361,9 @@ moe_status_t moe_measure_mma_peak(int32_t kind, int32_t iters, double* tflops);
  * no counterpart: they state no failure handling for the kernels. */
 moe_status_t moe_selftest_bounded_wait(int32_t limit_us, int32_t* done, moe_stream_t stream);
 
-/* Number of kernels the last moe_forward_ws / moe_forward call on this thread
- * enqueued (for launch accounting): 1 on the one-kernel decode path, 4 with at
+/* Number of kernels the last forward, gradient or operator around the forward
+ * on this thread enqueued (for launch accounting; 0 for an empty call).  For
+ * moe_forward_ws / moe_forward: 1 on the one-kernel decode path, 4 with at
  * most 32 routing slots otherwise, else 5, plus 2 when align runs its
  * multi-CTA form (more than 4096 slots). */
 int32_t moe_last_launch_count(void);

@@ -93,6 +93,12 @@ bool norm_shape_ok(const moe_tensor_t* t, float eps) {
     if (_s != MOE_OK) return _s;        \
   } while (0)
 
+// a call with nothing to do: no launches, and the count of them says so
+moe_status_t api_empty() {
+  api_set_launches(0);
+  return MOE_OK;
+}
+
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // rows of partial column sums of a norm's gradient, either way its rows are read
@@ -139,7 +145,7 @@ moe_status_t moe_norm_before(const moe_tensor_t* x, const moe_tensor_t* weight, 
   MOE_TRY(rows_of(out, g.T, g.H, true, &g.out));
   MOE_TRY(vector_of(weight, g.H, false, &g.w));
   MOE_TRY(rstd_of(rstd, g.T, true, &g.rstd, &g.rstd_s));
-  if (g.T == 0) return MOE_OK;
+  if (g.T == 0) return api_empty();
   int sms = 0;
   MOE_TRY(api_device(&sms, &g.ring.err));
   const bool wide = g.H % 8 == 0 && wide_ok(g.ring.in[0]) && wide_ok(g.out) && wide_ok(g.w);
@@ -173,7 +179,7 @@ moe_status_t moe_norm_after(const moe_tensor_t* y, const moe_tensor_t* residual,
   MOE_TRY(vector_of(next_weight, g.H, false, &g.wn));
   if (next_out) MOE_TRY(rows_of(next_out, g.T, g.H, true, &g.nxt));
   MOE_TRY(rstd_of(next_rstd, g.T, true, &g.next_rstd, &g.next_rstd_s));
-  if (g.T == 0) return MOE_OK;
+  if (g.T == 0) return api_empty();
   int sms = 0;
   MOE_TRY(api_device(&sms, &g.ring.err));
   const bool gate_rows = g.gate_mode == kGateFull || g.gate_mode == kGateChannel;
@@ -216,7 +222,7 @@ moe_status_t moe_norm_before_backward(const moe_tensor_t* dout, const moe_tensor
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < moe_norm_backward_workspace_bytes(g.T, g.H)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   }
-  if (g.T == 0 && !dweight) return MOE_OK;
+  if (g.T == 0 && !dweight) return api_empty();
   int sms = 0;
   MOE_TRY(api_device(&sms, &g.ring.err));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -274,7 +280,7 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < moe_norm_backward_workspace_bytes(g.T, g.H)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   }
-  if (g.T == 0 && !dweight && !gate_sum) return MOE_OK;
+  if (g.T == 0 && !dweight && !gate_sum) return api_empty();
   int sms = 0;
   MOE_TRY(api_device(&sms, &g.ring.err));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -322,7 +328,7 @@ moe_status_t moe_quantize_nvfp4(const moe_tensor_t* src, const moe_tensor_t* glo
   if (dst->sizes[0] != R || dst->sizes[1] != K || K % 32 != 0) return MOE_ERR_SHAPE_MISMATCH;
   const float* G = nullptr;
   MOE_TRY(scalar_of(global_scale, &G));
-  if (R == 0 || K == 0) return MOE_OK;
+  if (R == 0 || K == 0) return api_empty();
   if (!dst->data || !dst->scale) return MOE_ERR_INVALID_ARG;
   if (dst->strides[1] != 1 || dst->scale_strides[1] != 1) return MOE_ERR_UNSUPPORTED_LAYOUT;
   int sms = 0;
@@ -380,7 +386,7 @@ moe_status_t moe_linear_fp4(const moe_tensor_t* x, const moe_tensor_t* weight, i
   const LinearFp4Plan p = linear_fp4_plan(a.T, a.N, a.K, nv);
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < (p.total > 256 ? p.total : 256)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (a.T == 0) return MOE_OK;
+  if (a.T == 0) return api_empty();
   int sms = 0;
   MOE_TRY(api_device(&sms, &a.err));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -473,7 +479,7 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
   if (!layer_ws(T, H, I, E + shared_expert, k + shared_expert, wd, &L)) return MOE_ERR_INVALID_ARG;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (T == 0) return MOE_OK;
+  if (T == 0) return api_empty();
   int sms = 0;
   MOE_TRY(api_device(&sms, nullptr));
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -401,3 +401,18 @@ def test_without_the_norm_the_gradient_of_y_does_not_read_y(T, H, gate, act):
     ref = do.to(D) * w.to(D) * (1.0 if gt is None else act64(gt, act))
     assert bool(dy.isfinite().all())
     within(dy, ref, 2.0 ** -18 * ref.abs())
+
+
+def test_an_empty_call_launches_nothing_and_says_so():
+    w, e, x = torch.ones(64, device="cuda"), torch.empty(0, 64, dtype=BF, device="cuda"), torch.ones(2, 64, device="cuda")
+    r = torch.empty(0, device="cuda")
+    codes, sf, G = moe.quantize_nvfp4(x)
+    w13, w2 = moe.w13_from_packed(torch.zeros(4, 64, 64, dtype=BF, device="cuda")), torch.zeros(4, 64, 32, dtype=BF, device="cuda")
+    for call in (lambda: moe.norm_before(e, w), lambda: moe.norm_after(e, e, w, next_norm=True),
+                 lambda: moe.norm_before_backward(e, e, r), lambda: moe.norm_after_backward(e, e, r),
+                 lambda: moe.quantize_nvfp4(e, G), lambda: moe.linear_fp4(e, codes, sf, x_global=G),
+                 lambda: moe.layer_decode(e, torch.zeros(4, 64, device="cuda"), w13, w2, 2)):
+        moe.norm_before(x, w)
+        assert moe.last_launch_count() == 1
+        call()
+        assert moe.last_launch_count() == 0
