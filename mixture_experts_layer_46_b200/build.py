@@ -28,6 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 BINDING = os.path.join(PKG, "_moe_torch.so")
+BINDING_FOR = os.path.join(BUILD, "moe_torch.built_for")  # the torch and Python whose headers it was compiled with
 INCLUDE = os.path.join(ROOT, "include")
 
 CONFIG_CSV = os.path.join(PKG, "configs", "b200_tuned.csv")
@@ -151,7 +152,12 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     import torch
 
     src = os.path.join(CSRC, "moe_torch.cpp")
-    if not (force or _stale(BINDING, [src, os.path.join(INCLUDE, "moe.h")])):
+    built_for = f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+    same = False
+    if os.path.exists(BINDING_FOR):
+        with open(BINDING_FOR) as f:
+            same = f.read() == built_for
+    if same and not (force or _stale(BINDING, [src, os.path.join(INCLUDE, "moe.h")])):
         return BINDING
     base = os.path.dirname(torch.__file__)
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
@@ -166,6 +172,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    with open(BINDING_FOR, "w") as f:
+        f.write(built_for)
     return BINDING
 
 

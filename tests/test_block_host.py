@@ -297,3 +297,22 @@ def test_wrappers_pass_on_what_a_truth_value_raises():
                  lambda: moe.norm_after_backward(x, x, r, w, torch.zeros(1, 64), gate_grad=many)):
         with pytest.raises(RuntimeError, match="[Bb]oolean value"):
             call()
+
+
+def test_the_binding_is_compiled_again_for_another_torch(monkeypatch, tmp_path):
+    """Newer than its sources is not enough: its binary interface is that of the torch it was compiled with."""
+    from mixture_experts_layer_46_b200 import build
+
+    runs = []
+    monkeypatch.setattr(build, "BINDING_FOR", str(tmp_path / "built_for"))
+    monkeypatch.setattr(build, "_stale", lambda target, deps: False)
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, check: runs.append(cmd))
+    build.build_binding()
+    assert len(runs) == 1 and build.BINDING in runs[0]
+    build.build_binding()
+    assert len(runs) == 1
+    (tmp_path / "built_for").write_text("torch 0.0, another Python")
+    build.build_binding()
+    assert len(runs) == 2
+    build.build_binding(force=True)
+    assert len(runs) == 3
