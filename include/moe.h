@@ -560,9 +560,11 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
  *   x_global,      [1] or 0-d f32 on the device: the float scales of the e4m3 form (there x_global is
  *   weight_global  required, weight_global NULL = 1); NULL with e8m0 scales
  *   out            [T, N] bf16, any strides, rounded once from the fp32 sum
+ * An e8m0 scale of 255 is NaN, and so is every output of its weight row.
  * K % 32 == 0; T, N <= 2^24, K <= 2^20, T K and N K < 2^40.  Up to 16 tokens run as one launch where
- * (T - 1) N K <= 2^23 + 5120 K, else and with more as two (quantisation and placing of the scales;
- * the product on the tensor cores).  Sums are fp32 in a fixed order.  `workspace`:
+ * (T - 1) N K <= 2^23 + 5120 K and the quantised rows of min(T, 4) tokens fit a block's shared memory,
+ * min(T, 4) (K / 32) 72 <= 163840; else and with more tokens as two (quantisation and placing of the
+ * scales; the product on the tensor cores).  Sums are fp32 in a fixed order.  `workspace`:
  * moe_linear_fp4_workspace_bytes, 256-byte aligned (not touched by the one-launch form, which asks
  * for 256 bytes); it must not be shared by calls that run at the same time.  T = 0 is a
  * no-op.  Asynchronous on `stream`, no allocation. */

@@ -2,7 +2,7 @@
 // factors e2m1 codes with a scale per block of K (e8m0 per 32, or e4m3 per 16 times one float),
 // x quantised on the way in.
 //
-// Else (two launches):
+// Two forms, chosen by linear_fp4_by_rows.  With more than a few tokens or a large matrix, two launches:
 //   1. fp4_prepare: x -> codes [T, K/2] and scales, and the weight's scales, both placed in the
 //      128-row x 4-scale atoms that the tensor core reads (byte (row % 32) * 16 + (row / 32) * 4
 //      + scale), one contiguous run a k-step of 256 elements and tile.  Bound by the read of x.
@@ -14,10 +14,11 @@
 //      tenth fewer bytes a product and stall for its epilogue.  T = N = 8192, K = 4096: 106 us
 //      (5.2 PFLOP/s; 99 us with e8m0 scales): the products 81, the copies of the scales into
 //      tensor memory between them 16 (twelve a k-step, about 8 cycles each), loads 9, stores 7.
-// A few tokens of a matrix that is not large (one launch): the weights' bytes are the work; every block quantises
-// the few rows of x into shared memory, a warp takes a weight row at a time.  The products of
-// two e2m1 numbers are multiples of 1/4 of at most 36, so eight of them add up exactly in a
-// half; each block of 16 is then scaled and added in fp32.
+// With one token, or up to 16 of a matrix that is not large, one launch: every block quantises the
+// rows of x (four at most) into shared memory, a warp takes a weight row at a time.  The products of
+// two e2m1 numbers are multiples of 1/4 of at most 36, so eight of them add up exactly in a half;
+// each block of 16 is then scaled and added in fp32.  Bound by instructions (6.7 a weight and
+// thread) and a row's latency: 4096 x 4096, one token, 6.1 us at 11 % of DRAM.
 #include <atomic>
 
 #include "../../include/moe.h"

@@ -9,10 +9,11 @@
 // A cluster of CTAs takes a token, each CTA a share of the experts, and hands its logits
 // to all of them, so that every CTA ranks its experts against all others without another launch or
 // a counter in memory.  The choice between two experts must not hang on the order of additions,
-// so the sums carry their rounding errors along (x w and a bf16 weight's product with it are exact
-// in fp32) and meet in 64 bits; fp64 multiply-adds all the way took four times as long.  Latency
-// bounds the time otherwise: a warp takes 256 columns of eight experts at once, all loads in
-// flight together.  128 x 4096 router, one token: 7.4 us.
+// so the sums carry their rounding errors along and meet in 64 bits; fp64 multiply-adds all the way
+// took four times as long.  The terms are exact in fp32 (8 bits times 8 times 8) where pre_weight and
+// the router are bf16; an f32 pre_weight leaves the roundings of x w and of its product, an f32 router
+// takes the path in 64 bits.  Latency bounds the time otherwise: a warp takes 256 columns of eight
+// experts at once, all loads in flight together.  128 x 4096 router, one token: 7.4 us.
 #include <atomic>
 
 #include "../../include/moe.h"

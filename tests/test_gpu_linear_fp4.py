@@ -295,3 +295,16 @@ def test_linear_far_scales(T, ex, ew):
     assert bool((out[:, 0] == 0).all())
     want = torch.tensor(128.0, dtype=D) * 2.0 ** (ex + ew)
     assert bool((out[:, 1].cpu() == want.to(BF)).all())
+
+
+@pytest.mark.parametrize("form", ["nv", "mx"])
+@pytest.mark.parametrize("T,N,K,launches", [(1, 8, 72800, 1), (1, 8, 72832, 2), (2, 5, 36384, 1), (2, 5, 36416, 2),
+                                            (3, 7, 24256, 1), (3, 7, 24288, 2), (4, 24, 18176, 1), (4, 24, 18208, 2),
+                                            (16, 3, 18176, 1), (16, 3, 18208, 2)])
+def test_linear_on_both_sides_of_the_one_launch_forms_shared_memory(T, N, K, launches, form):
+    x = rows(T + N, T, K)
+    codes, sf, wg, wv = weight(K + N, N, K, form)
+    xg = (x.float().abs().max() / 2688.0).reshape(1) if form == "nv" else None
+    out = moe.linear_fp4(x, codes, sf, x_global=xg, w_global=wg)
+    assert moe.last_launch_count() == launches
+    check(out, nv64(x, xg)[2] if form == "nv" else mx64(x), wv)
