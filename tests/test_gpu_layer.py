@@ -299,3 +299,38 @@ def test_logits_that_are_not_finite_rank_last_in_every_layout(T, layout):
     # with more experts wanted than are finite, the others follow in the order of their indices
     _, ids, _ = moe.layer_decode(s["x"], router, moe.w13_from_packed(s["w13"]), s["w2"], E)
     assert bool((ids[:, 9:] == torch.tensor([3, 5, 9], dtype=torch.int32, device="cuda")).all())
+
+
+@pytest.mark.parametrize("T,k,shared,post,gate,act", [(1, 2, False, True, None, "none"), (4, 8, False, False, "token", "sigmoid"),
+                                                      (4, 3, True, True, "channel", "none"), (12, 2, False, True, "full", "tanh"),
+                                                      (32, 4, True, False, None, "none")])
+def test_mxfp4_experts_against_64_bit_formulas(T, k, shared, post, gate, act):
+    """The experts in 4 bits between the two ends, all in 64 bits but for the roundings that the form has
+    by definition (xn to bf16, xn and h to 4 bits).  Where those fall the other way a code moves by a
+    step: at most the forward's own bound, 6e-2 of its largest value (twice that after a norm), and
+    in root mean square 2^-6, with 2^-8 of the output besides."""
+    import oracle
+
+    H, I, E = 512, 256, 16
+    s = make(61 + T, T, H, I, E, shared)
+    c13, s13 = moe.quantize_mxfp4(s["w13"])
+    c2, s2 = moe.quantize_mxfp4(s["w2"])
+    g = torch.Generator().manual_seed(5)
+    shape = {None: None, "channel": (1, H), "token": (T, 1), "full": (T, H)}[gate]
+    gt = None if shape is None else torch.randn(*shape, generator=g).to(BF).cuda()
+    out, ids, p = moe.layer_decode(s["x"], s["router"], moe.w13_from_packed(c13, s13), c2, k, w2_scale=s2, pre_weight=s["pre"],
+                                   shared_expert=shared, post_norm=post, post_weight=s["post"] if post else None, gate=gt,
+                                   gate_act=act, residual_scale=0.5)
+    xn, wi, wp = route64(s["x"], s["pre"], s["router"], k, True, shared)
+    assert torch.equal(ids.long(), wi) and bool(((p.to(D) - wp).abs() <= 2.0 ** -20 * wp).all())
+    c, sc = c13.cpu(), s13.cpu()
+    z = oracle.moe_forward(xn.to(BF).cpu(), c[:, :I], c[:, I:], c2.cpu(), wi.int().cpu(), wp.float().cpu(),
+                           scales=(sc[:, :I], sc[:, I:], s2.cpu()))[0].to(D).cuda()
+    if post:
+        z = z / (z.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * s["post"].to(D)
+    if gt is not None:
+        z = z * act64(gt, act)
+    want = 0.5 * s["x"].to(D) + z
+    err, rms = (out.to(D) - want).abs(), lambda v: float(v.pow(2).mean().sqrt())
+    assert bool((err <= (2 if post else 1) * 6e-2 * z.abs().max() + HB * want.abs()).all())
+    assert rms(err) <= 2.0 ** -6 * rms(z) + HB * rms(want)
