@@ -197,18 +197,12 @@ _TENSOR = struct.Struct("=Qii4q4qQ4q").pack
 _PACKED_DT = tuple(getattr(torch, n) for n in ("uint8", "float4_e2m1fn_x2") if hasattr(torch, n))
 
 
-def _scale_bytes(t: torch.Tensor, scale: torch.Tensor) -> torch.Tensor:
-    """The e8m0 codes of packed e2m1 codes `t` as bytes (a wider type holds several): at least one for
-    every 32 elements of every row, or the library would read past their end."""
-    if scale.dtype == torch.float8_e4m3fn:
-        raise ValueError("e4m3 scales (one per 16 elements): expert weights take e8m0 codes, one per 32")
-    if scale.dtype != torch.uint8:
-        scale = scale.view(torch.uint8)
-    need = (*t.shape[:-1], 2 * t.shape[-1] // 32)
-    if scale.dim() != t.dim() or any(have < n for have, n in zip(scale.shape, need)):
-        raise ValueError(f"scales of shape {list(scale.shape)} (in bytes) for codes of shape {list(t.shape)}: "
-                         f"{list(need)} at least")
-    return scale
+def _check_scales(codes, scale) -> None:
+    """At least one e8m0 byte for every 32 elements (16 bytes of codes) of every row, or the library would
+    read past the scales' end."""
+    need = (*codes[:-1], codes[-1] // 16)
+    if len(scale) != len(need) or any(have < n for have, n in zip(scale, need)):
+        raise ValueError(f"scales of shape {list(scale)} (in bytes) for codes of shape {list(codes)}: {list(need)} at least")
 
 
 def desc(t: torch.Tensor, scale: torch.Tensor | None = None) -> MoeTensor:
@@ -218,7 +212,13 @@ def desc(t: torch.Tensor, scale: torch.Tensor | None = None) -> MoeTensor:
     if t.dtype in _PACKED_DT:
         if scale is None:
             raise ValueError("an e2m1 tensor needs its e8m0 scale tensor")
-        scale = _scale_bytes(t, scale)
+        if scale.dtype is not torch.uint8:  # (a wider type holds several codes)
+            if scale.dtype is torch.float8_e4m3fn:
+                raise ValueError("e4m3 scales (one per 16 elements): expert weights take e8m0 codes, one per 32")
+            scale = scale.view(torch.uint8)
+        z, q = t.shape, scale.shape
+        if not (len(z) == len(q) == 3 and q[2] * 16 >= z[2] and q[1] >= z[1] and q[0] >= z[0]):
+            _check_scales(z, q)  # (a matrix, or what is wrong)
         dt, sp, sq = MOE_E2M1X2, scale.data_ptr(), scale.stride()
     else:
         dt, sp, sq = _TORCH_DT.get(t.dtype, 99), 0, ()  # unknown dtypes are rejected by the library
