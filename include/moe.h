@@ -456,7 +456,8 @@ int32_t moe_builtin_config_count(void);
  *   normalize  0: the norm of y is left out (r_t = 1), weight and gate still apply
  *   rstd, next_rstd  [T] f32, any stride: r_t and r'_t (what the gradient reads); NULL: not wanted
  * out may be the same tensor (same strides) as x, y or residual; other overlaps are not
- * allowed.  eps finite and >= 0; squares are summed in fp32, so |x| has to stay below about 1e18.
+ * allowed.  eps finite and >= 0; squares are summed in fp32, so |x| has to stay below about 1e18, and with
+ * eps = 0 a row's largest above about 1e-16.
  * 1 <= H <= 16384; T = 0 is a no-op.  next_out needs no next_rstd and the other way round;
  * next_weight is read with next_out only.  Asynchronous on `stream`, no allocation, no state
  * between calls; every pointer is of the current device. */
@@ -519,6 +520,10 @@ moe_status_t moe_norm_after_backward(const moe_tensor_t* dout, const moe_tensor_
  * Kernels: the way in (norm, router, choice); the experts, with bf16 weights and few tokens two
  * kernels over their rows with xn and h in fp32, else the kernels of moe_forward; the gate and the
  * residual are part of the last one, with post_norm = 1 or MXFP4 weights a kernel of their own.
+ * Rounded to bf16 besides out: nothing in the two kernels over rows; in moe_forward's kernels xn and h,
+ * the tensor core's operands (to 4 bits with MXFP4 weights), each slot's weighted row, and with MXFP4
+ * weights y.  The same layer's result therefore changes by some 2^-9 of y where the token count leaves
+ * the kernels over rows.
  * Logits that are not finite (an infinity or a NaN in x's row, pre_weight or the router's row)
  * rank below every number and count as NaN in a softmax over all experts; with finite inputs the sum of
  * |x pre_weight router| over a row has to stay below 2^126.  Calls that take moe_forward's one-kernel
@@ -540,7 +545,7 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
  * Two forms of block scaling over e2m1 codes, by the scale_format argument:
  *   MOE_SCALE_E8M0_32  one e8m0 scale (2^(code - 127)) per 32 elements: moe_quantize_mxfp4's
  *                      (ROCm/aiter PR #3859, "Details": QuantType.per_1x32)
- *   MOE_SCALE_E4M3_16  one e4m3 scale per 16 elements, times one float for the whole tensor
+ *   MOE_SCALE_E4M3_16  one e4m3 scale (>= 0) per 16 elements, times one float for the whole tensor
  * In a MOE_E2M1X2 tensor of the second form `scale` points at the e4m3 codes.
  *
  * moe_quantize_nvfp4 writes the second form of the rows of src [R, K] (bf16 or f32, any

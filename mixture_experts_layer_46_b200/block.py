@@ -22,6 +22,9 @@ SCALE_E8M0_32, SCALE_E4M3_16 = 0, 1
 _DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.int32: MOE_I32, torch.int64: MOE_I64}
 
 
+# For calls of the C entry points through load(), such as the tests of their status codes; the functions
+# below go through the compiled module, which fills its own.
+
 def _desc(t: torch.Tensor | None):
     """The bytes of a moe_tensor_t (None stays NULL); unknown dtypes are rejected by the library."""
     if t is None:
@@ -171,7 +174,8 @@ def layer_decode(x, router, w13: MoeW13, w2, k: int, *, w2_scale=None, pre_weigh
 def quantize_nvfp4(src, global_scale=None, *, stream=None):
     """(codes uint8 [R, K/2], scales float8_e4m3fn [R, K/16], global_scale f32 [1]) of src [R, K]
     (bf16 or f32, K a multiple of 32): e2m1 codes, an e4m3 scale per 16, one float scale for the
-    tensor.  Without a given global_scale it is amax / 2688, which costs a pass over src."""
+    tensor.  Without a given global_scale it is amax / 2688, by torch: |src| written out and read back,
+    which costs more than the quantisation itself; keep the scale where src's range is known."""
     with contextlib.nullcontext() if stream is None else _on(stream, src):
         if global_scale is None:
             top = src.abs().amax().float() if src.numel() else torch.zeros((), device=src.device)
