@@ -301,6 +301,8 @@ __device__ __forceinline__ void down_rows(const DownArgs& g, const Group& sl, in
 
 // Blocks take equal runs of output rows; a block's warps take the (expert, 512 columns) pairs in
 // turn, each over all the block's rows.  part: [warp][row][T]
+// The first rows' weights (64 registers) live across the bodies for one, two and four slots: at 128
+// registers a thread spills 444 bytes.
 __global__ void __launch_bounds__(kThreads, 1) layer_down_kernel(const DownArgs g) {
   extern __shared__ __align__(16) float smem[];
   float* part = smem;

@@ -21,8 +21,9 @@
 // every blockDim-th element through the strides, which keeps a warp's accesses together.
 // Arithmetic is fp32 throughout; each output is rounded once, to its own type.
 //
-// Measured, H=4096 bf16: before 49 us and after + next 92 us at T=16384 (5.5 and 5.8 TB/s of the
-// 6.5 that a copy gets); the gradients 24 us each at T=4096 without their column sums.
+// Measured, H=4096 bf16: before 49 us and after + next 92 us at T=16384, each alone from a cold cache
+// (5.5 and 5.8 TB/s of the 6.5 that a copy gets; 139 us one after the other); the gradients 24 us each at
+// T=4096 without their column sums.
 #include <atomic>
 #include <initializer_list>
 
@@ -378,9 +379,9 @@ __device__ __forceinline__ float inv_root(float sum, float inv_h, float eps) {
 }
 
 // Threads of resident blocks on an SM, and rows on their way in a block's ring.  More of either
-// asks DRAM for too many streams at once: before + after + next at T=16384 H=4096 took 156 us with
-// 768 threads and four rows, 134 with 512 and four, 132 with 512 and three, 146 with two, 210
-// with 256.
+// asks DRAM for too many streams at once: before + after + next at T=16384 H=4096, compared on one
+// box, took 156 us with 768 threads and four rows, 134 with 512 and four, 132 with 512 and three, 146
+// with two, 210 with 256.
 constexpr int kResident = 512;
 constexpr int64_t kRingBytes = 96 << 10;  // of an SM's blocks together
 constexpr int min_blocks(int threads_per_sm, int max_threads) {
@@ -790,8 +791,10 @@ Shape shape_of(int64_t H, bool wide) {
   const int n = static_cast<int>((H + 7) / 8);
   // (two slots halve what a row costs besides its elements: T=16384 H=1024 after + next 41 -> 33 us;
   // through the strides, where an element is a load, one is faster: 1023 x 1407 f32 16 against 20)
-  // Rows of more than 8192 take four (512 threads; with 1024 and two the registers spill: T=4096
-  // H=16384 after + next 129 against 100 us); at H=4096 four are slower (92 against 104).
+  // Rows of more than 8192 take four on 512 threads.  That spills too (per thread, from the ring: none before
+  // and after, 60 bytes in the gradient before, 260 to 380 in the one after; up to 700 where two rows fit no
+  // ring), but less than two on 1024, with 64 registers: T=4096 H=16384 after + next 129 against 100 us.
+  // At H=4096 four are slower (92 against 104).
   const int vec = n <= (wide ? 64 : 256) ? 1 : wide && n > 1024 ? 4 : 2;
   Shape s;
   s.vec = vec;
