@@ -513,10 +513,10 @@ moe_status_t moe_layer_decode(const moe_tensor_t* x, const moe_tensor_t* pre_wei
   y.data = ws + L.y;
   // The experts' sum: finished where the slots are combined, or kept for the norm after it.  Off the
   // kernels over rows, xn and h are bf16 because the tensor core takes them so, and a slot's row because
-  // moe_forward's second product writes it so: in root mean square 0.0011 and 0.0007 of y for the two
-  // operands and 0.0007 for the rows, 0.0015 together, beside 0.0017 of out's own rounding (H = 4096,
-  // I = 1536, k = 8); fp32 rows would cost twice their traffic for a tenth of the sum of all four.  With
-  // MXFP4 weights the 4-bit operands are far coarser than y's bf16.
+  // moe_forward's second product writes it so.  Their errors in root mean square, of an out whose residual is
+  // twice its normed y: 0.0011, 0.0007 and 0.0007, with out's own 0.0017 together 0.0022 (H = 4096,
+  // I = 1536, k = 8); rows in fp32 would leave 0.0021 for twice their traffic.  With MXFP4 weights the
+  // 4-bit operands are far coarser than y's bf16.
   Finish f;
   const bool after = post_norm || wd != MOE_BF16;
   if (!after) {
