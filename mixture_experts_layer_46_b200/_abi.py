@@ -240,6 +240,14 @@ def _stream_ptr(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _scratch(workspace: torch.Tensor) -> tuple[int, int]:
+    """Address and bytes of a caller's workspace, one block of memory (an expanded tensor counts elements
+    that have no memory of their own)."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace is not contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def w13_from_packed(w13: torch.Tensor, scale: torch.Tensor | None = None) -> MoeW13:
     out = MoeW13()
     d = desc(w13, scale)
@@ -273,7 +281,7 @@ def forward(x, w13: MoeW13, w2, topk_ids, topk_weights, out=None, *, w2_scale=No
     if workspace is not None:
         rc = lib.moe_forward_ws(ctypes.byref(dx), ctypes.byref(w13), ctypes.byref(dw2),
                                 ctypes.byref(di), ctypes.byref(dw), ctypes.byref(do),
-                                workspace.data_ptr(), workspace.numel(), st)
+                                *_scratch(workspace), st)
         _check(rc, "moe_forward_ws")
     else:
         rc = lib.moe_forward(ctypes.byref(dx), ctypes.byref(w13), ctypes.byref(dw2),
@@ -321,7 +329,7 @@ def backward(x, w13: MoeW13, w2, w13t, w2t, topk_ids, topk_weights, dout, dx=Non
     g13 = ctypes.byref(desc(dw13)) if dw13 is not None else None
     g2 = ctypes.byref(desc(dw2)) if dw2 is not None else None
     rc = load().moe_backward_ws(ctypes.byref(d[0]), ctypes.byref(w13), *[ctypes.byref(v) for v in d[1:]],
-                                g13, g2, workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+                                g13, g2, *_scratch(workspace), _stream_ptr(stream))
     _check(rc, "moe_backward_ws")
     return dx, dweights, dw13, dw2
 
@@ -333,8 +341,7 @@ def backward_status(x, w13: MoeW13, w2, w13t, w2t, topk_ids, topk_weights, dout,
     g13 = ctypes.byref(desc(dw13)) if dw13 is not None else None
     g2 = ctypes.byref(desc(dw2)) if dw2 is not None else None
     st = _stream_ptr(stream) if torch.cuda.is_available() else None
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_n = workspace.numel() if workspace is not None else 0
+    ws_ptr, ws_n = _scratch(workspace) if workspace is not None else (None, 0)
     return int(load().moe_backward_ws(ctypes.byref(d[0]), ctypes.byref(w13), *[ctypes.byref(v) for v in d[1:]],
                                       g13, g2, ws_ptr, ws_n, st))
 
@@ -355,7 +362,7 @@ def backward_input(x, w13: MoeW13, w2, w13t, w2t, topk_ids, topk_weights, dout, 
         workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
     d = [desc(v) for v in (x, w2, w13t, w2t, topk_ids, topk_weights, dout, dx, dweights)]
     rc = load().moe_backward_input_ws(ctypes.byref(d[0]), ctypes.byref(w13), *[ctypes.byref(v) for v in d[1:]],
-                                      workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+                                      *_scratch(workspace), _stream_ptr(stream))
     _check(rc, "moe_backward_input_ws")
     return dx, dweights
 
@@ -366,8 +373,7 @@ def forward_status(x, w13: MoeW13, w2, topk_ids, topk_weights, out, *, w2_scale=
     dx, dw2, di, dw, do = desc(x), desc(w2, w2_scale), desc(topk_ids), desc(topk_weights), desc(out)
     lib = load()
     st = _stream_ptr(stream) if torch.cuda.is_available() else None
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_n = workspace.numel() if workspace is not None else 0
+    ws_ptr, ws_n = _scratch(workspace) if workspace is not None else (None, 0)
     return int(lib.moe_forward_ws(ctypes.byref(dx), ctypes.byref(w13), ctypes.byref(dw2),
                                   ctypes.byref(di), ctypes.byref(dw), ctypes.byref(do), ws_ptr,
                                   ws_n, st))
@@ -393,7 +399,7 @@ def forward_host(x_host, w13: MoeW13, w2, ids_host, weights_host, out_host, *, w
         return out_host
     rc = load().moe_forward_host_ws(ctypes.byref(dx), ctypes.byref(w13), ctypes.byref(dw2),
                                     ctypes.byref(di), ctypes.byref(dw), ctypes.byref(do),
-                                    workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+                                    *_scratch(workspace), _stream_ptr(stream))
     _check(rc, "moe_forward_host_ws")
     return out_host
 

@@ -325,3 +325,20 @@ def test_scale_tensors_are_bytes_and_cover_the_codes():
             moe.desc(codes, bad)
     with pytest.raises(ValueError, match="e4m3"):
         moe.desc(codes, raw.view(torch.float8_e4m3fn))
+
+
+def test_workspaces_that_are_not_one_block_of_memory_are_refused():
+    """An expanded or strided tensor's element count says nothing of the bytes behind its address."""
+    x, w13t, w2 = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(4, 64, 64, dtype=torch.bfloat16), \
+        torch.zeros(4, 64, 32, dtype=torch.bfloat16)
+    v, ids, wts = moe.w13_from_packed(w13t), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)
+    w2t = torch.zeros(4, 32, 64, dtype=torch.bfloat16)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 24), torch.zeros(1 << 22, dtype=torch.uint8)[::2]):
+        for call in (lambda: moe.forward(x, v, w2, ids, wts, workspace=ws, stream=0),
+                     lambda: moe.forward_status(x, v, w2, ids, wts, x.clone(), workspace=ws, stream=0),
+                     lambda: moe.forward_host(x, v, w2, ids, wts, x.clone(), workspace=ws, stream=0),
+                     lambda: moe.backward(x, v, w2, w13t, w2t, ids, wts, x, workspace=ws, stream=0),
+                     lambda: moe.backward_status(x, v, w2, w13t, w2t, ids, wts, x, x.clone(), wts.clone(), workspace=ws, stream=0),
+                     lambda: moe.backward_input(x, v, w2, w13t, w2t, ids, wts, x, workspace=ws, stream=0)):
+            with pytest.raises(ValueError, match="contiguous"):
+                call()
